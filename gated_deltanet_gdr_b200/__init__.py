@@ -10,6 +10,10 @@ binding's functions raises: there is no fallback.
     out, state_pool  = recurrent_step(q, k, v, beta, g, gk, state_pool, ssm_state_indices,
                                       actual_seq_lengths, num_accepted_tokens, scale)
 
+Beside the rule: the causal conv1d before it (``conv1d``, ``conv1d_bwd``), the gated linear recurrence with one scalar
+state per channel (``scan_fwd``, ``scan_bwd``, ``scan_step``), and the slots of the state pools (``slot_copy``,
+``slot_fork``, ``slot_compact``, ``slot_free``).
+
 Layouts are BNSD: q, k (B, Nk, S, Dk); v (B, Nv, S, Dv); beta, g (B, Nv, S).
 """
 from __future__ import annotations
@@ -32,6 +36,8 @@ DEVERR_SLOT_INDEX, DEVERR_LENGTH, DEVERR_TIMEOUT = 0x1, 0x2, 0x4
 
 # Every symbol the C header declares (checked by the ABI test).
 EXPORTED = ("gdr_chunk_fwd_workspace", "gdr_chunk_fwd", "gdr_chunk_fwd_noalloc", "gdr_recurrent_step", "gdr_recurrent_step_spec", "gdr_conv1d",
+            "gdr_conv1d_bwd", "gdr_conv1d_bwd_workspace", "gdr_scan_fwd", "gdr_scan_bwd", "gdr_scan_step",
+            "gdr_slot_copy", "gdr_slot_fork", "gdr_slot_compact", "gdr_slot_free",
             "gdr_prologue_apply", "gdr_get_error", "gdr_debug_set_wait_limit", "gdr_debug_timeout_site",
             "gdr_debug_set_chunk_schedule",
             "gdr_status_string", "gdr_version")
@@ -40,6 +46,10 @@ EXPORTED = ("gdr_chunk_fwd_workspace", "gdr_chunk_fwd", "gdr_chunk_fwd_noalloc",
 class GdrPrologueStruct(ctypes.Structure):
     _fields_ = [("l2norm_qk", ctypes.c_int), ("eps", ctypes.c_float), ("beta_logits", ctypes.c_int),
                 ("A_log", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p)]
+
+
+class GdrPoolStruct(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("slot_bytes", ctypes.c_size_t)]
 
 
 class GdrEpilogueStruct(ctypes.Structure):
@@ -79,6 +89,25 @@ def lib() -> ctypes.CDLL:
         L.gdr_recurrent_step_spec.argtypes = L.gdr_recurrent_step.argtypes
         L.gdr_conv1d.restype = i32
         L.gdr_conv1d.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp]
+        L.gdr_conv1d_bwd.restype = i32
+        L.gdr_conv1d_bwd.argtypes = [vp] * 9 + [i32] * 8 + [vp] * 5 + [ctypes.c_size_t, vp]
+        L.gdr_conv1d_bwd_workspace.restype = ctypes.c_size_t
+        L.gdr_conv1d_bwd_workspace.argtypes = [i32] * 7
+        L.gdr_scan_fwd.restype = i32
+        L.gdr_scan_fwd.argtypes = [vp] * 4 + [i32] * 7 + [vp] * 4
+        L.gdr_scan_bwd.restype = i32
+        L.gdr_scan_bwd.argtypes = [vp] * 6 + [i32] * 7 + [vp] * 4
+        L.gdr_scan_step.restype = i32
+        L.gdr_scan_step.argtypes = [vp, vp, vp, i32, vp, vp, vp] + [i32] * 8 + [vp, vp]
+        pools = ctypes.POINTER(GdrPoolStruct)
+        L.gdr_slot_copy.restype = i32
+        L.gdr_slot_copy.argtypes = [pools, i32, i32, vp, vp, i32, vp]
+        L.gdr_slot_fork.restype = i32
+        L.gdr_slot_fork.argtypes = [pools, i32, i32, vp, vp, i32, vp, vp]
+        L.gdr_slot_compact.restype = i32
+        L.gdr_slot_compact.argtypes = [pools, i32, i32, vp, vp, vp, vp]
+        L.gdr_slot_free.restype = i32
+        L.gdr_slot_free.argtypes = [pools, i32, i32, vp, i32, vp, vp]
         L.gdr_prologue_apply.restype = i32
         L.gdr_prologue_apply.argtypes = [vp, vp, vp, vp, vp, vp, f32, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp,
                                          vp]
@@ -411,6 +440,314 @@ def prepare_conv1d(x, weight, bias=None, conv_state=None, actual_seq_lengths=Non
     args, res = _conv1d_checked(x, weight, bias, conv_state, actual_seq_lengths, Nk, Nv, Dk, Dv, q, k, v,
                                 conv_state_out, output_state, stream)
     return PreparedCall(lib().gdr_conv1d, args, "gdr_conv1d", res)
+
+
+# ---- the conv1d's gradient, the gated linear recurrence and the state slots -------------------------------------
+#
+# These calls marshal for short kernels (a decode step, a handful of slots), so each looks at the current device and
+# stream once and passes plain integers to the C entry.  With ``stream=`` another than the current stream, the tensors
+# a call allocates belong to that stream, and the allocator is told which streams use what (``_uses``).
+
+class _Call:
+    """The device and stream of one call, and the tensors it touches."""
+    __slots__ = ("dev", "stream", "other", "used")
+
+    def __init__(self, stream):
+        self.dev = torch.cuda.current_device()
+        current = torch.cuda.current_stream()
+        self.other = None
+        if stream is not None and stream.cuda_stream != current.cuda_stream:
+            if stream.device.index != self.dev:
+                raise RuntimeError(f"the stream is on {stream.device}, but the call runs on the current device "
+                                   f"cuda:{self.dev}")
+            self.other, current = stream, stream
+        self.stream = current.cuda_stream
+        self.used = []
+
+    def ptr(self, t, name, dtype, shape):
+        """Address of a dense tensor of that type and shape on the current device; None for None."""
+        if t is None:
+            return None
+        if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or not t.is_cuda \
+                or t.device.index != self.dev or not t.is_contiguous():
+            _dev(t, name, dtype, shape)  # says which of them
+        if self.other is not None:
+            self.used.append(t)
+        return t.data_ptr()
+
+    def new(self, shape, dtype):
+        if self.other is None:
+            return torch.empty(shape, dtype=dtype, device=self.dev)
+        with torch.cuda.stream(self.other):
+            t = torch.empty(shape, dtype=dtype, device=self.dev)
+        t.record_stream(torch.cuda.current_stream())
+        return t
+
+    def done(self, status, what):
+        for t in self.used:
+            t.record_stream(self.other)
+        if status != GDR_OK:
+            _check(status, what)
+
+
+def _four(x, name):
+    if not isinstance(x, torch.Tensor) or x.dim() != 4:
+        raise ValueError(f"{name} must be a (B, N, S, D) tensor")
+    return x.shape
+
+
+def _gate_code(x, g):
+    if not isinstance(g, torch.Tensor) or (g.dtype != torch.float32 and g.dtype != x.dtype):
+        raise RuntimeError("g must be a float32 tensor or have the dtype of x")
+    return _dtype_code(g.dtype)
+
+
+def scan_checkpoint_shape(B: int, N: int, S: int, D: int):
+    """Shape of the fp32 ``checkpoints`` of ``scan_fwd``: the state before every 64th token."""
+    return (B, N, (S + 63) // 64, D)
+
+
+def _scan_fwd_args(x, g, initial_state, actual_seq_lengths, mix, out, final_state, output_final_state, checkpoints,
+                   output_checkpoints, stream):
+    B, N, S, D = _four(x, "x")
+    dt, code = x.dtype, _dtype_code(x.dtype)
+    gcode = _gate_code(x, g)
+    c = _Call(stream)
+    px, pg = c.ptr(x, "x", dt, x.shape), c.ptr(g, "g", g.dtype, x.shape)
+    pi = c.ptr(initial_state, "initial_state", torch.float32, (B, N, D))
+    pl = c.ptr(actual_seq_lengths, "actual_seq_lengths", torch.int32, (B,))
+    if out is None:
+        out = c.new((B, N, S, D), dt)
+    if final_state is None and output_final_state:
+        final_state = c.new((B, N, D), torch.float32)
+    if checkpoints is None and output_checkpoints:
+        checkpoints = c.new(scan_checkpoint_shape(B, N, S, D), torch.float32)
+    args = (px, pg, pi, pl, B, N, S, D, code, gcode, int(bool(mix)), c.ptr(out, "out", dt, (B, N, S, D)),
+            c.ptr(final_state, "final_state", torch.float32, (B, N, D)),
+            c.ptr(checkpoints, "checkpoints", torch.float32, scan_checkpoint_shape(B, N, S, D)), c.stream)
+    return c, args, (out, final_state, checkpoints)
+
+
+def scan_fwd(x, g, initial_state=None, actual_seq_lengths=None, *, mix: bool = False, out=None, final_state=None,
+             output_final_state: bool = True, checkpoints=None, output_checkpoints: bool = False, stream=None):
+    """Gated linear recurrence over a sequence (``gdr_scan_fwd``): h_t = exp(g_t) h_{t-1} + x_t per channel, or
+    + (1 - exp(g_t)) x_t with ``mix``.
+
+    x (B, N, S, D) in fp32, bf16 or fp16, g (B, N, S, D) log-decay in fp32 or the dtype of x, initial_state fp32
+    (B, N, D) or None.  Returns (out, final_state or None, checkpoints or None); ``output_checkpoints`` keeps the fp32
+    states that ``scan_bwd`` needs.  ``final_state`` may be ``initial_state`` (in-place update)."""
+    c, args, res = _scan_fwd_args(x, g, initial_state, actual_seq_lengths, mix, out, final_state, output_final_state,
+                                  checkpoints, output_checkpoints, stream)
+    c.done(lib().gdr_scan_fwd(*args), "gdr_scan_fwd")
+    return res
+
+
+def prepare_scan_fwd(x, g, initial_state=None, actual_seq_lengths=None, *, mix: bool = False, out=None,
+                     final_state=None, output_final_state: bool = True, checkpoints=None,
+                     output_checkpoints: bool = False, stream=None) -> PreparedCall:
+    """Check and marshal a gdr_scan_fwd call once; see scan_fwd for the arguments."""
+    c, args, res = _scan_fwd_args(x, g, initial_state, actual_seq_lengths, mix, out, final_state, output_final_state,
+                                  checkpoints, output_checkpoints, stream)
+    c.done(GDR_OK, "gdr_scan_fwd")
+    return PreparedCall(lib().gdr_scan_fwd, args, "gdr_scan_fwd", res)
+
+
+def scan_bwd(x, g, checkpoints, dout, dfinal_state=None, actual_seq_lengths=None, *, mix: bool = False, dx=None,
+             dg=None, dinitial_state=None, output_dinitial_state: bool = True, stream=None):
+    """Gradient of ``scan_fwd`` (``gdr_scan_bwd``) from the checkpoints it kept, for the gradients dout (B, N, S, D) of
+    out and dfinal_state (B, N, D) of final_state.  Returns (dx, dg, dinitial_state or None)."""
+    B, N, S, D = _four(x, "x")
+    dt, code = x.dtype, _dtype_code(x.dtype)
+    gcode = _gate_code(x, g)
+    c = _Call(stream)
+    px, pg = c.ptr(x, "x", dt, x.shape), c.ptr(g, "g", g.dtype, x.shape)
+    pc = c.ptr(checkpoints, "checkpoints", torch.float32, scan_checkpoint_shape(B, N, S, D))
+    pd = c.ptr(dout, "dout", dt, x.shape)
+    pf = c.ptr(dfinal_state, "dfinal_state", torch.float32, (B, N, D))
+    pl = c.ptr(actual_seq_lengths, "actual_seq_lengths", torch.int32, (B,))
+    if dx is None:
+        dx = c.new((B, N, S, D), dt)
+    if dg is None:
+        dg = c.new((B, N, S, D), g.dtype)
+    if dinitial_state is None and output_dinitial_state:
+        dinitial_state = c.new((B, N, D), torch.float32)
+    st = lib().gdr_scan_bwd(px, pg, pc, pd, pf, pl, B, N, S, D, code, gcode, int(bool(mix)),
+                            c.ptr(dx, "dx", dt, x.shape), c.ptr(dg, "dg", g.dtype, x.shape),
+                            c.ptr(dinitial_state, "dinitial_state", torch.float32, (B, N, D)), c.stream)
+    c.done(st, "gdr_scan_bwd")
+    return dx, dg, dinitial_state
+
+
+def _scan_step_args(x, g, state_pool, ssm_state_indices, actual_seq_lengths, num_accepted_tokens, mix, out, per_token,
+                    stream):
+    B, N, S, D = _four(x, "x")
+    dt, code = x.dtype, _dtype_code(x.dtype)
+    gcode = _gate_code(x, g)
+    if not isinstance(state_pool, torch.Tensor) or state_pool.dim() != 3:
+        raise ValueError("state_pool must be a (slots, N, D) tensor")
+    if not isinstance(ssm_state_indices, torch.Tensor) or ssm_state_indices.numel() != B * S:
+        raise ValueError("ssm_state_indices must hold B * S int32 slot indices, one per flattened token")
+    slots = state_pool.shape[0]
+    c = _Call(stream)
+    px, pg = c.ptr(x, "x", dt, x.shape), c.ptr(g, "g", g.dtype, x.shape)
+    pp = c.ptr(state_pool, "state_pool", torch.float32, (slots, N, D))
+    ps = c.ptr(ssm_state_indices, "ssm_state_indices", torch.int32, ssm_state_indices.shape)
+    pl = c.ptr(actual_seq_lengths, "actual_seq_lengths", torch.int32, (B,))
+    pa = c.ptr(num_accepted_tokens, "num_accepted_tokens", torch.int32, (B,))
+    if out is None:
+        out = c.new((B, N, S, D), dt)
+    args = (px, pg, pp, slots, ps, pl, pa, B, N, S, D, code, gcode, int(bool(mix)), int(bool(per_token)),
+            c.ptr(out, "out", dt, x.shape), c.stream)
+    return c, args, (out, state_pool)
+
+
+def scan_step(x, g, state_pool, ssm_state_indices, actual_seq_lengths=None, num_accepted_tokens=None, *,
+              mix: bool = False, out=None, per_token: bool = False, stream=None):
+    """The recurrence for decode over a pool of fp32 states (slots, N, D) (``gdr_scan_step``), updating it in place:
+    x, g (B, N, S, D) with S <= 8, index and length arrays as in ``recurrent_step``.  Returns (out, state_pool)."""
+    c, args, res = _scan_step_args(x, g, state_pool, ssm_state_indices, actual_seq_lengths, num_accepted_tokens, mix,
+                                   out, per_token, stream)
+    c.done(lib().gdr_scan_step(*args), "gdr_scan_step")
+    return res
+
+
+def prepare_scan_step(x, g, state_pool, ssm_state_indices, actual_seq_lengths=None, num_accepted_tokens=None, *,
+                      mix: bool = False, out=None, per_token: bool = False, stream=None) -> PreparedCall:
+    """Check and marshal a gdr_scan_step call once; see scan_step for the arguments."""
+    c, args, res = _scan_step_args(x, g, state_pool, ssm_state_indices, actual_seq_lengths, num_accepted_tokens, mix,
+                                   out, per_token, stream)
+    c.done(GDR_OK, "gdr_scan_step")
+    return PreparedCall(lib().gdr_scan_step, args, "gdr_scan_step", res)
+
+
+def conv1d_bwd_workspace_bytes(B: int, S: int, Nk: int, Nv: int, Dk: int, Dv: int, K: int) -> int:
+    """Bytes of workspace ``gdr_conv1d_bwd`` needs for these sizes."""
+    return int(lib().gdr_conv1d_bwd_workspace(B, S, Nk, Nv, Dk, Dv, K))
+
+
+def conv1d_bwd(x, weight, dq, dk, dv, bias=None, conv_state=None, actual_seq_lengths=None, dconv_state_out=None, *,
+               dx=None, dweight=None, dbias=None, dconv_state=None, workspace=None, stream=None):
+    """Gradient of ``conv1d`` (``gdr_conv1d_bwd``) for the gradients dq, dk (B, Nk, S, Dk) and dv (B, Nv, S, Dv) of its
+    outputs and dconv_state_out (B, C, K) or None of its new state.  Returns (dx (B, S, C), dweight fp32 (C, K), dbias
+    fp32 (C,), dconv_state (B, C, K)); ``workspace`` (uint8) is allocated per call when not given."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 3 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("x must be (B, S, C) and weight (C, K)")
+    B, S, C = x.shape
+    K = weight.shape[1]
+    _, Nk, _, Dk = _four(dq, "dq")
+    _, Nv, _, Dv = _four(dv, "dv")
+    if C != 2 * Nk * Dk + Nv * Dv:
+        raise ValueError(f"x has {C} channels; 2 * Nk * Dk + Nv * Dv = {2 * Nk * Dk + Nv * Dv}")
+    dt, code = x.dtype, _dtype_code(x.dtype)
+    c = _Call(stream)
+    ins = (c.ptr(x, "x", dt, x.shape), c.ptr(weight, "weight", dt, (C, K)), c.ptr(bias, "bias", dt, (C,)),
+           c.ptr(conv_state, "conv_state", dt, (B, C, K)),
+           c.ptr(actual_seq_lengths, "actual_seq_lengths", torch.int32, (B,)), c.ptr(dq, "dq", dt, (B, Nk, S, Dk)),
+           c.ptr(dk, "dk", dt, (B, Nk, S, Dk)), c.ptr(dv, "dv", dt, (B, Nv, S, Dv)),
+           c.ptr(dconv_state_out, "dconv_state_out", dt, (B, C, K)))
+    need = conv1d_bwd_workspace_bytes(B, S, Nk, Nv, Dk, Dv, K)
+    if workspace is None:
+        workspace = c.new((need,), torch.uint8) if need else None
+    elif workspace.numel() < need:
+        raise ValueError(f"workspace holds {workspace.numel()} bytes; the call needs {need}")
+    if dx is None:
+        dx = c.new((B, S, C), dt)
+    if dweight is None:
+        dweight = c.new((C, K), torch.float32)
+    if dbias is None:
+        dbias = c.new((C,), torch.float32)
+    if dconv_state is None:
+        dconv_state = c.new((B, C, K), dt)
+    st = lib().gdr_conv1d_bwd(*ins, B, S, Nk, Nv, Dk, Dv, K, code, c.ptr(dx, "dx", dt, (B, S, C)),
+                              c.ptr(dweight, "dweight", torch.float32, (C, K)),
+                              c.ptr(dbias, "dbias", torch.float32, (C,)),
+                              c.ptr(dconv_state, "dconv_state", dt, (B, C, K)),
+                              c.ptr(workspace, "workspace", torch.uint8, None if workspace is None else workspace.shape),
+                              0 if workspace is None else workspace.numel(), c.stream)
+    c.done(st, "gdr_conv1d_bwd")
+    return dx, dweight, dbias, dconv_state
+
+
+def _pools(c, pools):
+    """The C array of a list of pools (tensors whose first dimension is the slots), and their number of slots."""
+    pools = [pools] if isinstance(pools, torch.Tensor) else list(pools)
+    if not pools:
+        raise ValueError("pools must name at least one tensor")
+    arr = (GdrPoolStruct * len(pools))()
+    slots = None
+    for i, t in enumerate(pools):
+        if not isinstance(t, torch.Tensor) or t.dim() < 1:
+            raise ValueError("a pool must be a tensor whose first dimension is the slots")
+        if slots is None:
+            slots = t.shape[0]
+        elif t.shape[0] != slots:
+            raise ValueError(f"all pools must have {slots} slots, pool {i} has {t.shape[0]}")
+        arr[i].data = c.ptr(t, f"pools[{i}]", t.dtype, t.shape)
+        arr[i].slot_bytes = t.element_size() * (t.numel() // slots if slots else 0)
+    return arr, len(pools), slots
+
+
+def _list_i32(c, t, name, n=None):
+    if not isinstance(t, torch.Tensor) or t.dim() != 1:
+        raise ValueError(f"{name} must be a one-dimensional int32 tensor")
+    return c.ptr(t, name, torch.int32, t.shape if n is None else (n,))
+
+
+def slot_copy(pools, src, dst, *, stream=None):
+    """pool[dst[i]] = pool[src[i]] in every pool (``gdr_slot_copy``).  ``pools``: one tensor (slots, ...) or a list of
+    up to 64 of any types with the same number of slots; src, dst int32 (n), -1 for no move.  A move whose target is
+    another move's source or an earlier move's target is skipped and flagged (``get_error``).  Returns pools."""
+    c = _Call(stream)
+    arr, n_pools, slots = _pools(c, pools)
+    ps = _list_i32(c, src, "src")
+    st = lib().gdr_slot_copy(arr, n_pools, slots, ps, _list_i32(c, dst, "dst", src.shape[0]), src.shape[0], c.stream)
+    c.done(st, "gdr_slot_copy")
+    return pools
+
+
+def slot_fork(pools, slot_table, parents, *, new_slot_table=None, stream=None):
+    """Beam reordering (``gdr_slot_fork``): row i continues from row parents[i] (-1: from nothing).  The lowest
+    child of a row keeps its slot, the others get copies in the slots of the rows without a child.  Returns the
+    new slot of every row (int32)."""
+    c = _Call(stream)
+    arr, n_pools, slots = _pools(c, pools)
+    pt = _list_i32(c, slot_table, "slot_table")
+    n = slot_table.shape[0]
+    pp = _list_i32(c, parents, "parents", n)
+    if new_slot_table is None:
+        new_slot_table = c.new((n,), torch.int32)
+    st = lib().gdr_slot_fork(arr, n_pools, slots, pt, pp, n, _list_i32(c, new_slot_table, "new_slot_table", n), c.stream)
+    c.done(st, "gdr_slot_fork")
+    return new_slot_table
+
+
+def slot_compact(pools, live, *, new_slot=None, n_live=None, stream=None):
+    """Moves the live slots (live int32 (slots), non-zero) at or above their count into the free slots below it
+    (``gdr_slot_compact``).  Returns (new_slot int32 (slots): where each slot went, -1 for free ones; n_live int32
+    (1,))."""
+    c = _Call(stream)
+    arr, n_pools, slots = _pools(c, pools)
+    pl = _list_i32(c, live, "live", slots)
+    if new_slot is None:
+        new_slot = c.new((slots,), torch.int32)
+    if n_live is None:
+        n_live = c.new((1,), torch.int32)
+    st = lib().gdr_slot_compact(arr, n_pools, slots, pl, _list_i32(c, new_slot, "new_slot", slots),
+                                _list_i32(c, n_live, "n_live", 1), c.stream)
+    c.done(st, "gdr_slot_compact")
+    return new_slot, n_live
+
+
+def slot_free(pools, idx, live=None, *, stream=None):
+    """Sets the slots idx (int32 (n), -1 for none) of every pool to zero and, with ``live``, marks them free
+    (``gdr_slot_free``).  Returns pools."""
+    c = _Call(stream)
+    arr, n_pools, slots = _pools(c, pools)
+    pi = _list_i32(c, idx, "idx")
+    pl = None if live is None else _list_i32(c, live, "live", slots)
+    st = lib().gdr_slot_free(arr, n_pools, slots, pi, idx.shape[0], pl, c.stream)
+    c.done(st, "gdr_slot_free")
+    return pools
 
 
 def prologue(q=None, k=None, b=None, a=None, A_log=None, dt_bias=None, eps: float = 1e-6, *, stream=None):

@@ -143,24 +143,25 @@ bool copy_i32(std::vector<int32_t> &h, const int32_t *d, size_t n, cudaStream_t 
 }
 
 // lengths within [0, S]
-int check_lengths_host(const int32_t *lengths, int B, int S, cudaStream_t s) {
+int check_lengths_host(const int32_t *lengths, int B, int S, cudaStream_t s) try {
     if (!lengths) return GDR_OK;
     std::vector<int32_t> L;
     if (!copy_i32(L, lengths, (size_t)B, s)) return GDR_ERR_LAUNCH;
     for (int b = 0; b < B; ++b)
         if (L[b] < 0 || L[b] > S) return GDR_ERR_SHAPE;
     return GDR_OK;
+} catch (...) {  // no memory for the copies: no exception leaves a C entry
+    return GDR_ERR_LAUNCH;
 }
 
 // Decode: lengths in [0, S], accepted counts in range, every slot a sequence reads or writes in [0, slots), and
 // no slot touched by two sequences.  per_token selects the speculative-decoding reading (the chain starts at token
 // A - 1's slot and every processed token's state goes to its own slot); otherwise the chain starts at token 0's
 // slot and the first min(A, L) states are committed.
-int check_decode_host(const int32_t *idx, const int32_t *lengths, const int32_t *accepted, int B, int S, int slots,
-                      int per_token, cudaStream_t s) {
-    std::vector<int32_t> I, L, A;
-    if (!copy_i32(I, idx, (size_t)B * S, s) || !copy_i32(L, lengths, (size_t)B, s) ||
-        !copy_i32(A, accepted, accepted ? (size_t)B : 0, s))
+int check_decode_lists(const int32_t *idx, const std::vector<int32_t> &L, const int32_t *accepted, int B, int S,
+                       int slots, int per_token, cudaStream_t s) try {
+    std::vector<int32_t> I, A;
+    if (!copy_i32(I, idx, (size_t)B * S, s) || !copy_i32(A, accepted, accepted ? (size_t)B : 0, s))
         return GDR_ERR_LAUNCH;
     std::unordered_map<int32_t, int> owner;
     for (int b = 0; b < B; ++b) {
@@ -186,7 +187,39 @@ int check_decode_host(const int32_t *idx, const int32_t *lengths, const int32_t 
         }
     }
     return GDR_OK;
+} catch (...) {
+    return GDR_ERR_LAUNCH;
 }
+
+int check_decode_host(const int32_t *idx, const int32_t *lengths, const int32_t *accepted, int B, int S, int slots,
+                      int per_token, cudaStream_t s) try {
+    std::vector<int32_t> L;
+    if (!lengths) L.assign((size_t)B, S);  // every sequence has S tokens
+    else if (!copy_i32(L, lengths, (size_t)B, s)) return GDR_ERR_LAUNCH;
+    return check_decode_lists(idx, L, accepted, B, S, slots, per_token, s);
+} catch (...) {
+    return GDR_ERR_LAUNCH;
+}
+
+// Whether no output shares bytes with an input or another output (spans without a pointer or without bytes share none)
+struct Span {
+    const void *p;
+    unsigned long long n;
+};
+bool overlap(const Span &a, const Span &b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return x && y && a.n && b.n && x < y + b.n && y < x + a.n;
+}
+template <int NO, int NI> bool disjoint(const Span (&outs)[NO], const Span (&ins)[NI]) {
+    for (int i = 0; i < NO; ++i) {
+        for (int j = 0; j < NI; ++j)
+            if (overlap(outs[i], ins[j])) return false;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i], outs[j])) return false;
+    }
+    return true;
+}
+unsigned long long elt(int dtype) { return dtype == GDR_F32 ? 4 : 2; }
 
 int check_epilogue(const gdr_epilogue *e) {
     if (!e) return GDR_OK;
@@ -360,6 +393,243 @@ extern "C" int gdr_conv1d(const void *x, const void *weight, const void *bias, c
     return e == cudaSuccess ? GDR_OK : GDR_ERR_LAUNCH;
 }
 
+extern "C" size_t gdr_conv1d_bwd_workspace(int B, int S, int Nk, int Nv, int Dk, int Dv, int K) {
+    if (check_common(B, Nk, Nv, S, Dk, Dv, GDR_F32) != GDR_OK || K < 1 || K > 8) return 0;
+    return conv1d_bwd_workspace(B, S, 2 * Nk * Dk + Nv * Dv, K);
+}
+
+extern "C" int gdr_conv1d_bwd(const void *x, const void *weight, const void *bias, const void *conv_state_in,
+                              const int32_t *actual_seq_lengths, const void *dq, const void *dk, const void *dv,
+                              const void *dconv_state_out, int B, int S, int Nk, int Nv, int Dk, int Dv, int K,
+                              gdr_dtype dtype, void *dx, float *dweight, float *dbias, void *dconv_state_in,
+                              void *workspace, size_t ws_bytes, gdr_stream_t stream) {
+    int st = check_common(B, Nk, Nv, S, Dk, Dv, dtype);
+    if (st) return st;
+    if (K < 1 || K > 8) return GDR_ERR_SHAPE;
+    if (B > 65535 || (long long)S > 65535LL * 64) return GDR_ERR_SHAPE;  // as gdr_conv1d
+    if (!dweight) return GDR_ERR_NULL;
+    if ((long long)B * S > 0 && (!x || !weight || !dq || !dk || !dv || !dx)) return GDR_ERR_NULL;
+    if (B > 0 && dconv_state_in && !weight) return GDR_ERR_NULL;
+    const void *ptrs[] = {x, weight, bias, conv_state_in, actual_seq_lengths, dq, dk, dv, dconv_state_out, dx, dweight,
+                          dbias, dconv_state_in, workspace};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return GDR_ERR_ALIGN;
+    const size_t need = gdr_conv1d_bwd_workspace(B, S, Nk, Nv, Dk, Dv, K);
+    if (need > 0 && !workspace) return GDR_ERR_NULL;
+    if (ws_bytes < need) return GDR_ERR_WORKSPACE;
+    const unsigned long long C = 2ull * Nk * Dk + 1ull * Nv * Dv, e = elt(dtype), qk = e * B * Nk * S * Dk;
+    const Span ins[] = {{x, e * B * S * C}, {weight, e * C * K}, {bias, e * C}, {conv_state_in, e * B * C * K},
+                        {actual_seq_lengths, 4ull * B}, {dq, qk}, {dk, qk}, {dv, e * B * Nv * S * Dv},
+                        {dconv_state_out, e * B * C * K}};
+    const Span outs[] = {{dx, e * B * S * C}, {dweight, 4 * C * K}, {dbias, 4 * C}, {dconv_state_in, e * B * C * K},
+                         {workspace, need}};
+    if (!disjoint(outs, ins)) return GDR_ERR_SHAPE;
+    unsigned int *err = nullptr;
+    if ((st = device_setup(&err))) return st;
+    ConvBwdArgs a{};
+    a.x = x; a.w = weight; a.bias = bias; a.state_in = conv_state_in; a.lengths = actual_seq_lengths;
+    a.dq = dq; a.dk = dk; a.dv = dv; a.dstate_out = dconv_state_out;
+    a.dx = dx; a.dw = dweight; a.db = dbias; a.dstate_in = dconv_state_in;
+    a.partial = need > 0 ? static_cast<float *>(workspace) : nullptr;
+    a.B = B; a.S = S; a.C = 2 * Nk * Dk + Nv * Dv; a.Nk = Nk; a.Nv = Nv; a.Dk = Dk; a.Dv = Dv;
+    a.err = err;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (checks_enabled() && (st = check_lengths_host(actual_seq_lengths, B, S, cs))) return st;
+    return launch_conv1d_bwd(a, K, dtype, cs) == cudaSuccess ? GDR_OK : GDR_ERR_LAUNCH;
+}
+
+namespace {
+int check_scan(int B, int N, int S, int D, int dtype, int gate_dtype, int mode) {
+    if (dtype != GDR_F32 && dtype != GDR_BF16 && dtype != GDR_F16) return GDR_ERR_DTYPE;
+    if (gate_dtype != GDR_F32 && gate_dtype != dtype) return GDR_ERR_DTYPE;
+    if (mode != GDR_SCAN_ADD && mode != GDR_SCAN_MIX) return GDR_ERR_SHAPE;
+    if (B < 0 || S < 0 || N < 1 || D < 1) return GDR_ERR_SHAPE;
+    // channels are counted in 31 bits (grids, channel indices); offsets into the tensors are 64-bit
+    if ((long long)B * N >= (1LL << 31) || (long long)B * N * D >= (1LL << 31)) return GDR_ERR_SHAPE;
+    if ((long long)N * D >= (1LL << 31) || (double)B * N * D * S >= 0x1p60) return GDR_ERR_SHAPE;
+    return GDR_OK;
+}
+}  // namespace
+
+extern "C" int gdr_scan_fwd(const void *x, const void *g, const float *initial_state,
+                            const int32_t *actual_seq_lengths, int B, int N, int S, int D, gdr_dtype dtype,
+                            gdr_dtype gate_dtype, int mode, void *out, float *final_state, float *checkpoints,
+                            gdr_stream_t stream) {
+    int st = check_scan(B, N, S, D, dtype, gate_dtype, mode);
+    if (st) return st;
+    if ((long long)B * S > 0 && (!x || !g || !out)) return GDR_ERR_NULL;
+    const void *ptrs[] = {x, g, initial_state, actual_seq_lengths, out, final_state, checkpoints};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return GDR_ERR_ALIGN;
+    const unsigned long long rows = (unsigned long long)B * N, all = rows * S * D, state = rows * D * 4;
+    const Span ins[] = {{x, all * elt(dtype)}, {g, all * elt(gate_dtype)},
+                        {initial_state == final_state ? nullptr : initial_state, state},
+                        {actual_seq_lengths, 4ull * B}};
+    const Span outs[] = {{out, all * elt(dtype)}, {final_state, state},
+                         {checkpoints, state * ((S + kChunk - 1ull) / kChunk)}};
+    if (!disjoint(outs, ins)) return GDR_ERR_SHAPE;
+    if (B == 0 || (S == 0 && !final_state)) return GDR_OK;
+    unsigned int *err = nullptr;
+    if ((st = device_setup(&err))) return st;
+    ScanArgs a{};
+    a.x = x; a.g = g; a.initial_state = initial_state; a.lengths = actual_seq_lengths;
+    a.B = B; a.N = N; a.S = S; a.D = D; a.mode = mode;
+    a.out = out; a.final_state = final_state; a.checkpoints = checkpoints; a.err = err;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (checks_enabled() && (st = check_lengths_host(actual_seq_lengths, B, S, cs))) return st;
+    return launch_scan_fwd(a, dtype, gate_dtype, cs) == cudaSuccess ? GDR_OK : GDR_ERR_LAUNCH;
+}
+
+extern "C" int gdr_scan_bwd(const void *x, const void *g, const float *checkpoints, const void *dout,
+                            const float *dfinal_state, const int32_t *actual_seq_lengths, int B, int N, int S, int D,
+                            gdr_dtype dtype, gdr_dtype gate_dtype, int mode, void *dx, void *dg,
+                            float *dinitial_state, gdr_stream_t stream) {
+    int st = check_scan(B, N, S, D, dtype, gate_dtype, mode);
+    if (st) return st;
+    if ((long long)B * S > 0 && (!x || !g || !checkpoints || !dout || !dx || !dg)) return GDR_ERR_NULL;
+    const void *ptrs[] = {x, g, checkpoints, dout, dfinal_state, actual_seq_lengths, dx, dg, dinitial_state};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return GDR_ERR_ALIGN;
+    const unsigned long long rows = (unsigned long long)B * N, all = rows * S * D, state = rows * D * 4;
+    const Span ins[] = {{x, all * elt(dtype)}, {g, all * elt(gate_dtype)},
+                        {checkpoints, state * ((S + kChunk - 1ull) / kChunk)}, {dout, all * elt(dtype)},
+                        {dfinal_state == dinitial_state ? nullptr : dfinal_state, state},
+                        {actual_seq_lengths, 4ull * B}};
+    const Span outs[] = {{dx, all * elt(dtype)}, {dg, all * elt(gate_dtype)}, {dinitial_state, state}};
+    if (!disjoint(outs, ins)) return GDR_ERR_SHAPE;
+    if (B == 0 || (S == 0 && !dinitial_state)) return GDR_OK;
+    unsigned int *err = nullptr;
+    if ((st = device_setup(&err))) return st;
+    ScanBwdArgs a{};
+    a.x = x; a.g = g; a.checkpoints = checkpoints; a.dout = dout; a.dfinal_state = dfinal_state;
+    a.lengths = actual_seq_lengths;
+    a.B = B; a.N = N; a.S = S; a.D = D; a.mode = mode;
+    a.dx = dx; a.dg = dg; a.dinitial_state = dinitial_state; a.err = err;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (checks_enabled() && (st = check_lengths_host(actual_seq_lengths, B, S, cs))) return st;
+    return launch_scan_bwd(a, dtype, gate_dtype, cs) == cudaSuccess ? GDR_OK : GDR_ERR_LAUNCH;
+}
+
+extern "C" int gdr_scan_step(const void *x, const void *g, float *state_pool, int slots,
+                             const int32_t *ssm_state_indices, const int32_t *actual_seq_lengths,
+                             const int32_t *num_accepted_tokens, int B, int N, int S, int D, gdr_dtype dtype,
+                             gdr_dtype gate_dtype, int mode, int per_token, void *out, gdr_stream_t stream) {
+    int st = check_scan(B, N, S, D, dtype, gate_dtype, mode);
+    if (st) return st;
+    if (S < 1 || S > kDecodeMaxTokens || slots < 1 || (double)slots * N * D >= 0x1p60) return GDR_ERR_SHAPE;
+    if (B > 0 && (!x || !g || !state_pool || !ssm_state_indices || !out)) return GDR_ERR_NULL;
+    const void *ptrs[] = {x, g, state_pool, ssm_state_indices, actual_seq_lengths, num_accepted_tokens, out};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return GDR_ERR_ALIGN;
+    const unsigned long long all = (unsigned long long)B * N * S * D;
+    const Span ins[] = {{x, all * elt(dtype)}, {g, all * elt(gate_dtype)}, {ssm_state_indices, 4ull * B * S},
+                        {actual_seq_lengths, 4ull * B}, {num_accepted_tokens, 4ull * B}};
+    const Span outs[] = {{out, all * elt(dtype)}, {state_pool, 4ull * slots * N * D}};
+    if (!disjoint(outs, ins)) return GDR_ERR_SHAPE;
+    if (B == 0) return GDR_OK;
+    unsigned int *err = nullptr;
+    if ((st = device_setup(&err))) return st;
+    ScanStepArgs a{};
+    a.x = x; a.g = g; a.pool = state_pool; a.slots = slots;
+    a.idx = ssm_state_indices; a.lengths = actual_seq_lengths; a.accepted = num_accepted_tokens;
+    a.B = B; a.N = N; a.S = S; a.D = D; a.mode = mode; a.per_token = per_token != 0;
+    a.out = out; a.err = err;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (checks_enabled() && (st = check_decode_host(ssm_state_indices, actual_seq_lengths, num_accepted_tokens, B, S,
+                                                    slots, a.per_token, cs)))
+        return st;
+    return launch_scan_step(a, dtype, gate_dtype, cs) == cudaSuccess ? GDR_OK : GDR_ERR_LAUNCH;
+}
+
+namespace {
+// the pools of a slot call, checked and copied into the kernels' argument block
+int take_pools(const gdr_pool *pools, int n_pools, int slots, long long max_slots, SlotPools *out) {
+    if (n_pools < 1 || n_pools > GDR_MAX_POOLS || slots < 1 || slots > max_slots) return GDR_ERR_SHAPE;
+    if (!pools) return GDR_ERR_NULL;
+    *out = SlotPools{};
+    for (int i = 0; i < n_pools; ++i) {
+        if (!pools[i].data) return GDR_ERR_NULL;
+        if (!aligned16(pools[i].data)) return GDR_ERR_ALIGN;
+        if (pools[i].slot_bytes < 1 || pools[i].slot_bytes > (1ull << 38)) return GDR_ERR_SHAPE;
+        out->data[i] = static_cast<char *>(pools[i].data);
+        out->bytes[i] = pools[i].slot_bytes;
+    }
+    // pools that share bytes would be moved twice, in no order
+    for (int i = 0; i < n_pools; ++i)
+        for (int j = 0; j < i; ++j) {
+            const char *a = out->data[i], *b = out->data[j];
+            if (a < b + out->bytes[j] * (unsigned long long)slots && b < a + out->bytes[i] * (unsigned long long)slots)
+                return GDR_ERR_SHAPE;
+        }
+    out->n = n_pools;
+    out->slots = slots;
+    return GDR_OK;
+}
+
+constexpr long long kMaxSlots = (1LL << 24) - 1;
+}  // namespace
+
+extern "C" int gdr_slot_copy(const gdr_pool *pools, int n_pools, int slots, const int32_t *src, const int32_t *dst,
+                             int n, gdr_stream_t stream) {
+    SlotPools p;
+    int st = take_pools(pools, n_pools, slots, kMaxSlots, &p);
+    if (st) return st;
+    if (n < 0 || n > kMaxSlotMoves) return GDR_ERR_SHAPE;
+    if (n > 0 && (!src || !dst)) return GDR_ERR_NULL;
+    if (!aligned16(src) || !aligned16(dst)) return GDR_ERR_ALIGN;
+    if (n == 0) return GDR_OK;
+    if ((st = device_setup(&p.err))) return st;
+    return launch_slot_copy(p, src, dst, n, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? GDR_OK
+                                                                                                  : GDR_ERR_LAUNCH;
+}
+
+extern "C" int gdr_slot_fork(const gdr_pool *pools, int n_pools, int slots, const int32_t *slot_table,
+                             const int32_t *parents, int n, int32_t *new_slot_table, gdr_stream_t stream) {
+    SlotPools p;
+    int st = take_pools(pools, n_pools, slots, kMaxSlots, &p);
+    if (st) return st;
+    if (n < 0 || n > kMaxForkRows) return GDR_ERR_SHAPE;
+    if (n > 0 && (!slot_table || !parents || !new_slot_table)) return GDR_ERR_NULL;
+    if (!aligned16(slot_table) || !aligned16(parents) || !aligned16(new_slot_table)) return GDR_ERR_ALIGN;
+    // every block reads both inputs while one writes the result
+    if (n > 0 && (new_slot_table < slot_table + n && slot_table < new_slot_table + n)) return GDR_ERR_SHAPE;
+    if (n > 0 && (new_slot_table < parents + n && parents < new_slot_table + n)) return GDR_ERR_SHAPE;
+    if (n == 0) return GDR_OK;
+    if ((st = device_setup(&p.err))) return st;
+    return launch_slot_fork(p, slot_table, parents, n, new_slot_table, reinterpret_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess ? GDR_OK : GDR_ERR_LAUNCH;
+}
+
+extern "C" int gdr_slot_compact(const gdr_pool *pools, int n_pools, int slots, const int32_t *live, int32_t *new_slot,
+                                int32_t *n_live, gdr_stream_t stream) {
+    SlotPools p;
+    int st = take_pools(pools, n_pools, slots, kMaxCompactSlots, &p);
+    if (st) return st;
+    if (!live || !new_slot || !n_live) return GDR_ERR_NULL;
+    if (!aligned16(live) || !aligned16(new_slot) || !aligned16(n_live)) return GDR_ERR_ALIGN;
+    if (new_slot < live + slots && live < new_slot + slots) return GDR_ERR_SHAPE;
+    if (n_live >= live && n_live < live + slots) return GDR_ERR_SHAPE;
+    if (n_live >= new_slot && n_live < new_slot + slots) return GDR_ERR_SHAPE;
+    if ((st = device_setup(&p.err))) return st;
+    return launch_slot_compact(p, live, new_slot, n_live, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GDR_OK : GDR_ERR_LAUNCH;
+}
+
+extern "C" int gdr_slot_free(const gdr_pool *pools, int n_pools, int slots, const int32_t *idx, int n, int32_t *live,
+                             gdr_stream_t stream) {
+    SlotPools p;
+    int st = take_pools(pools, n_pools, slots, kMaxSlots, &p);
+    if (st) return st;
+    if (n < 0 || n > kMaxSlotMoves) return GDR_ERR_SHAPE;
+    if (n > 0 && !idx) return GDR_ERR_NULL;
+    if (!aligned16(idx) || !aligned16(live)) return GDR_ERR_ALIGN;
+    if (n > 0 && live && idx < live + slots && live < idx + n) return GDR_ERR_SHAPE;
+    if (n == 0) return GDR_OK;
+    if ((st = device_setup(&p.err))) return st;
+    return launch_slot_free(p, idx, n, live, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? GDR_OK
+                                                                                                   : GDR_ERR_LAUNCH;
+}
+
 extern "C" int gdr_prologue_apply(const void *q, const void *k, const void *b, const float *a, const float *A_log,
                                   const float *dt_bias, float eps, int B, int Nk, int Nv, int S, int Dk,
                                   gdr_dtype dtype, void *q_hat, void *k_hat, void *beta, float *g,
@@ -413,7 +683,7 @@ extern "C" const char *gdr_status_string(int status) {
         case GDR_ERR_UNSUPPORTED: return "head size not built (Dk and Dv must be 16, 32, 64 or 128)";
         case GDR_ERR_DEVICE: return "no usable sm_100 CUDA device";
         case GDR_ERR_LAUNCH: return "a CUDA call or kernel launch failed";
-        case GDR_ERR_WORKSPACE: return "workspace smaller than gdr_chunk_fwd_workspace() returns";
+        case GDR_ERR_WORKSPACE: return "workspace smaller than the call's workspace query returns";
         default: return "unknown status";
     }
 }

@@ -105,6 +105,73 @@ cudaError_t launch_gated_rmsnorm(void *out, const void *z, const float *norm_w, 
 cudaError_t launch_conv1d(const void *x, const void *weight, const void *bias, const void *state_in,
                           const int32_t *lengths, int B, int S, int Nk, int Nv, int Dk, int Dv, int K, gdr_dtype dt,
                           void *q, void *k, void *v, void *state_out, unsigned int *err, cudaStream_t s);
+// gradient of the conv1d (gdr_conv1d_bwd): fp32 partial sums of dweight and dbias per (b, time tile) in the workspace,
+// added up in a fixed order by a second kernel
+struct ConvBwdArgs {
+    const void *x, *w, *bias, *state_in;
+    const int32_t *lengths;
+    const void *dq, *dk, *dv, *dstate_out;
+    void *dx;
+    float *dw, *db;
+    void *dstate_in;
+    float *partial;
+    int B, S, C, Nk, Nv, Dk, Dv;
+    unsigned int *err;
+};
+size_t conv1d_bwd_workspace(int B, int S, int C, int K);
+cudaError_t launch_conv1d_bwd(const ConvBwdArgs &a, int K, gdr_dtype dt, cudaStream_t s);
+
+// the gated linear recurrence (gdr_scan_fwd, gdr_scan_bwd, gdr_scan_step)
+struct ScanArgs {
+    const void *x, *g;
+    const float *initial_state;
+    const int32_t *lengths;
+    int B, N, S, D, mode;
+    void *out;
+    float *final_state, *checkpoints;
+    unsigned int *err;
+};
+struct ScanBwdArgs {
+    const void *x, *g;
+    const float *checkpoints;
+    const void *dout;
+    const float *dfinal_state;
+    const int32_t *lengths;
+    int B, N, S, D, mode;
+    void *dx, *dg;
+    float *dinitial_state;
+    unsigned int *err;
+};
+struct ScanStepArgs {
+    const void *x, *g;
+    float *pool;
+    int slots;
+    const int32_t *idx, *lengths, *accepted;
+    int B, N, S, D, mode, per_token;
+    void *out;
+    unsigned int *err;
+};
+cudaError_t launch_scan_fwd(const ScanArgs &a, gdr_dtype dt, gdr_dtype gt, cudaStream_t s);
+cudaError_t launch_scan_bwd(const ScanBwdArgs &a, gdr_dtype dt, gdr_dtype gt, cudaStream_t s);
+cudaError_t launch_scan_step(const ScanStepArgs &a, gdr_dtype dt, gdr_dtype gt, cudaStream_t s);
+
+// slots of the state pools (gdr_slot_copy, gdr_slot_fork, gdr_slot_compact, gdr_slot_free)
+constexpr int kMaxSlotMoves = 65536;    // moves of one copy or free
+constexpr int kMaxForkRows = 16384;     // rows of one fork
+constexpr int kMaxCompactSlots = 262144;  // slots of one compaction
+struct SlotPools {
+    char *data[GDR_MAX_POOLS];
+    unsigned long long bytes[GDR_MAX_POOLS];  // of one slot
+    int n, slots;
+    unsigned int *err;
+};
+cudaError_t launch_slot_copy(const SlotPools &p, const int32_t *src, const int32_t *dst, int n, cudaStream_t s);
+cudaError_t launch_slot_fork(const SlotPools &p, const int32_t *table, const int32_t *parents, int n,
+                             int32_t *new_table, cudaStream_t s);
+cudaError_t launch_slot_compact(const SlotPools &p, const int32_t *live, int32_t *new_slot, int32_t *n_live,
+                                cudaStream_t s);
+cudaError_t launch_slot_free(const SlotPools &p, const int32_t *idx, int n, int32_t *live, cudaStream_t s);
+
 cudaError_t launch_prologue(const void *q, const void *k, const void *b, const float *a, const float *A_log,
                             const float *dt_bias, float eps, int B, int Nk, int Nv, int S, int Dk, gdr_dtype dt,
                             void *q_hat, void *k_hat, void *beta, float *g, cudaStream_t stream);

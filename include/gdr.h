@@ -79,13 +79,14 @@ typedef enum gdr_status {
     GDR_ERR_UNSUPPORTED = 5, /* valid per the API but not built: Dk or Dv not in {16,32,64,128} */
     GDR_ERR_DEVICE = 6,      /* no usable device, or it is not sm_100 */
     GDR_ERR_LAUNCH = 7,      /* a kernel launch or a CUDA call failed */
-    GDR_ERR_WORKSPACE = 8    /* ws_bytes is smaller than gdr_chunk_fwd_workspace() returns */
+    GDR_ERR_WORKSPACE = 8    /* ws_bytes is smaller than the call's workspace query returns */
 } gdr_status;
 
 typedef enum gdr_dtype { GDR_F32 = 0, GDR_BF16 = 1, GDR_F16 = 2 } gdr_dtype;
 
 /* Bits of the device error word (gdr_get_error). */
-#define GDR_DEVERR_SLOT_INDEX 0x1u /* a referenced slot index was outside [0, slots) */
+#define GDR_DEVERR_SLOT_INDEX 0x1u /* a referenced slot index was outside [0, slots), or the slot operators'
+                                      targets collided */
 #define GDR_DEVERR_LENGTH 0x2u     /* a length was outside [0, S] */
 #define GDR_DEVERR_TIMEOUT 0x4u    /* a kernel's bounded wait for its own copies or for another of its warp
                                       groups ran out: it released what it held and returned early, so the
@@ -323,6 +324,176 @@ int gdr_recurrent_step_spec(const void *q, const void *k, const void *v, const v
 int gdr_conv1d(const void *x, const void *weight, const void *bias, const void *conv_state_in,
                const int32_t *actual_seq_lengths, int B, int S, int Nk, int Nv, int Dk, int Dv, int K,
                gdr_dtype dtype, void *q, void *k, void *v, void *conv_state_out, gdr_stream_t stream);
+
+/*
+ * Gradient of gdr_conv1d.  With pre[t, c] = bias[c] + sum_j weight[c, j] x[t - K + 1 + j, c] (the positions before
+ * 0 from conv_state_in) and y = silu(pre), for t < L_b:
+ *     dpre[t]      = dy[t] * s (1 + pre (1 - s)),  s = 1 / (1 + e^{-pre})
+ *     dx[t]        = sum_j weight[c, j] dpre[t + K - 1 - j]   (dpre = 0 behind the sequence)
+ *     dweight[c,j] = sum_{b, t < L_b} dpre[t] x[t - K + 1 + j],   dbias[c] = sum_{b, t < L_b} dpre[t]
+ * and the gradient of the history entries before position 0 is that of conv_state_in.
+ *
+ *   x, weight, bias, conv_state_in, actual_seq_lengths   as given to gdr_conv1d
+ *   dq, dk, dv           device: the gradients of gdr_conv1d's q, k, v, in their layouts; padding rows are ignored
+ *   dconv_state_out      device (B, C, K) or NULL (zero): the gradient of gdr_conv1d's conv_state_out
+ *   dx                   device (B, S, C), written in full; rows t >= L_b are zero
+ *   dweight, dbias       device fp32 (C, K) and (C); dbias may be NULL.  Summed in fp32 in a fixed order, so equal
+ *                        calls give equal bits
+ *   dconv_state_in       device (B, C, K) or NULL: not written
+ *   workspace, ws_bytes  device scratch of at least gdr_conv1d_bwd_workspace() bytes (the partial sums of dweight and
+ *                        dbias), owned by the caller, 16-byte aligned; two calls in flight at once need separate ones
+ * Everything but dweight and dbias is in dtype.  No output may overlap an input.  Constraints, and the length check,
+ * as for gdr_conv1d; a sequence whose length is outside [0, S] contributes nothing (its dx and dconv_state_in rows
+ * are zero).  A shorter workspace returns GDR_ERR_WORKSPACE.
+ */
+int gdr_conv1d_bwd(const void *x, const void *weight, const void *bias, const void *conv_state_in,
+                   const int32_t *actual_seq_lengths, const void *dq, const void *dk, const void *dv,
+                   const void *dconv_state_out, int B, int S, int Nk, int Nv, int Dk, int Dv, int K, gdr_dtype dtype,
+                   void *dx, float *dweight, float *dbias, void *dconv_state_in, void *workspace, size_t ws_bytes,
+                   gdr_stream_t stream);
+
+/* Bytes of workspace a gdr_conv1d_bwd call of these sizes needs (0 for invalid sizes and where there is nothing to sum). */
+size_t gdr_conv1d_bwd_workspace(int B, int S, int Nk, int Nv, int Dk, int Dv, int K);
+
+/*
+ * Gated linear recurrence: the diagonal relative of the rule, one scalar state per channel (the recurrence
+ * h_t = a_t h_{t-1} + b_t of the lecture module's sequential_scan and parallel_scan).  For every sequence b, head n and
+ * channel d, with a_t = exp(g_t):
+ *     GDR_SCAN_ADD:  h_t = a_t h_{t-1} + x_t
+ *     GDR_SCAN_MIX:  h_t = a_t h_{t-1} + (1 - a_t) x_t
+ *     out_t = h_t
+ * The state is fp32 always, whatever the inputs' type: a slowly decaying state takes many writes that are small next
+ * to it, and a 16-bit state would drop them.
+ *
+ *   x                    device (B, N, S, D) in dtype (a channels-last (B, S, C) tensor is N = 1, D = C)
+ *   g                    device (B, N, S, D) log-decay in gate_dtype: GDR_F32 or dtype.  -infinity forgets the state
+ *                        exactly (a boundary between packed sequences).  Not range-checked: values above 0 grow the
+ *                        state, and a run of tokens whose factors multiply past fp32 gives infinities or NaN
+ *   initial_state        device fp32 (B, N, D) or NULL: zeros
+ *   actual_seq_lengths   device int32 (B) or NULL: all S.  Tokens t >= L_b are padding: their contents are ignored
+ *                        and their out rows are zero.  L_b = 0 gives final_state = initial_state exactly
+ *   out                  device (B, N, S, D) in dtype, written in full
+ *   final_state          device fp32 (B, N, D) or NULL: the state after token L_b - 1.  May alias initial_state
+ *   checkpoints          device fp32 (B, N, ceil(S / 64), D) or NULL: the state before token 64 c of each chunk c, for
+ *                        gdr_scan_bwd.  Chunks with 64 c >= L_b (c > 0) are left as they were
+ * Apart from final_state, no output may overlap an input.  Constraints: B, S >= 0; N, D >= 1; B * N * D < 2^31; any D
+ * (sizes that are a multiple of 4 are faster); pointers 16-byte aligned.  A length outside [0, S] skips the sequence
+ * (out rows zero, final_state and checkpoints as they were) and sets GDR_DEVERR_LENGTH.
+ */
+#define GDR_SCAN_ADD 0
+#define GDR_SCAN_MIX 1
+int gdr_scan_fwd(const void *x, const void *g, const float *initial_state, const int32_t *actual_seq_lengths, int B,
+                 int N, int S, int D, gdr_dtype dtype, gdr_dtype gate_dtype, int mode, void *out, float *final_state,
+                 float *checkpoints, gdr_stream_t stream);
+
+/*
+ * Gradient of gdr_scan_fwd.  With lambda_t the gradient of h_t (lambda_t = dout_t + mu_{t+1}, mu_t = a_t lambda_t, and
+ * mu_{L_b} = dfinal_state):
+ *     ADD:  dx_t = lambda_t                dg_t = mu_t h_{t-1}
+ *     MIX:  dx_t = (1 - a_t) lambda_t      dg_t = mu_t (h_{t-1} - x_t)
+ *     dinitial_state = mu_0
+ * The states h are computed again from x, g and the checkpoints, which costs no more traffic than reading out back
+ * and keeps them in fp32.
+ *
+ *   x, g, actual_seq_lengths, mode   as given to gdr_scan_fwd
+ *   checkpoints          as gdr_scan_fwd wrote them for these inputs (required when S > 0)
+ *   dout                 device (B, N, S, D) in dtype; padding rows are ignored
+ *   dfinal_state         device fp32 (B, N, D) or NULL: zeros
+ *   dx, dg               device (B, N, S, D) in dtype and in gate_dtype, written in full; padding rows are zero
+ *   dinitial_state       device fp32 (B, N, D) or NULL: not written.  L_b = 0 gives dfinal_state exactly
+ * No output may overlap an input, but dinitial_state may alias dfinal_state.  Other constraints as for gdr_scan_fwd.  A
+ * sequence whose length is outside [0, S] gets zero gradients and sets GDR_DEVERR_LENGTH.
+ */
+int gdr_scan_bwd(const void *x, const void *g, const float *checkpoints, const void *dout, const float *dfinal_state,
+                 const int32_t *actual_seq_lengths, int B, int N, int S, int D, gdr_dtype dtype, gdr_dtype gate_dtype,
+                 int mode, void *dx, void *dg, float *dinitial_state, gdr_stream_t stream);
+
+/*
+ * The recurrence for decode, over a pool of state slots: what gdr_recurrent_step is to gdr_chunk_fwd, with the same
+ * readings of the index and length arrays.
+ *
+ *   x, g, out            as for gdr_scan_fwd
+ *   state_pool           device fp32 (slots, N, D), read and updated in place.  Slots no token commits to are left
+ *                        byte-identical
+ *   ssm_state_indices    device int32 (B * S): the slot of every token
+ *   actual_seq_lengths   device int32 (B) or NULL: all S
+ *   num_accepted_tokens  device int32 (B) or NULL
+ *   per_token            0: the chain starts from the slot of token 0 and the state after token t is committed to the
+ *                        slot of token t for t < min(A_b, L_b) (A_b = L_b when num_accepted_tokens is NULL).
+ *                        1: the speculative reading of gdr_recurrent_step_spec: the chain starts from the slot of
+ *                        token A_b - 1 (A_b in [1, S]; 1 when NULL) and every processed token's state goes to its own
+ *                        slot
+ * Two sequences must not reference the same slot.  Constraints: 1 <= S <= 8, slots >= 1, others as for gdr_scan_fwd.  A
+ * sequence with a bad slot, length or accepted count is skipped (out rows zero, pool untouched) and flagged, as in
+ * gdr_recurrent_step.
+ */
+int gdr_scan_step(const void *x, const void *g, float *state_pool, int slots, const int32_t *ssm_state_indices,
+                  const int32_t *actual_seq_lengths, const int32_t *num_accepted_tokens, int B, int N, int S, int D,
+                  gdr_dtype dtype, gdr_dtype gate_dtype, int mode, int per_token, void *out, gdr_stream_t stream);
+
+/*
+ * Slots of the state pools: copying, forking, compacting and freeing.  A decode step rewrites a sequence's whole state
+ * in place, so two sequences cannot share a slot the way they can share the pages of a growing cache: a fork is a
+ * copy, and what can be saved is the copies that need not be made, and the launches.  One call serves up to
+ * GDR_MAX_POOLS pools with the same slot numbering (the matrix states, conv windows and recurrent states of several
+ * layers).
+ *
+ *   data        device, slots * slot_bytes bytes, slot s at data + s * slot_bytes; 16-byte aligned
+ *   slot_bytes  bytes of one slot, >= 1 (a multiple of 16 is fastest)
+ * The array of gdr_pool is in host memory and is read before the call returns; the pools must not overlap.
+ */
+#define GDR_MAX_POOLS 64
+typedef struct gdr_pool {
+    void *data;
+    size_t slot_bytes;
+} gdr_pool;
+
+/*
+ * pool[dst[i]] = pool[src[i]] for i < n, in every pool (a prefix's state handed to new sequences).
+ *   src, dst   device int32 (n).  An entry of -1 in either is no move (the unused end of a fixed-size list); src[i] =
+ *              dst[i] is none either.  Several moves may share a source.
+ * A move with another index outside [0, slots) is skipped.  So is a move whose target is another move's source or an
+ * earlier move's target (the copies run at once, so its result would depend on their order).  Both set
+ * GDR_DEVERR_SLOT_INDEX.  Constraints: 1 <= n_pools <= GDR_MAX_POOLS, 1 <= slots < 2^24, 0 <= n <= 65536.
+ */
+int gdr_slot_copy(const gdr_pool *pools, int n_pools, int slots, const int32_t *src, const int32_t *dst, int n,
+                  gdr_stream_t stream);
+
+/*
+ * Beam reordering with the fewest copies: row i of the batch continues from row parents[i].
+ *   slot_table      device int32 (n): the slot of every row, all different
+ *   parents         device int32 (n): in [0, n), or -1: the row continues from nothing (its slot's contents are left
+ *                   as they are)
+ *   new_slot_table  device int32 (n), written in full; a permutation of slot_table.  May overlap neither input
+ * The lowest row that continues from row p keeps p's slot and nothing is copied for it.  The other rows, in ascending
+ * order, take the slots of the rows that nobody continues from, in ascending order of those rows, and their parent's
+ * state is copied there.
+ * A parent outside [-1, n) counts as -1.  A copy whose slots are outside [0, slots), or whose target is the slot of
+ * another row too, is skipped.  Both set GDR_DEVERR_SLOT_INDEX.  Constraints: as for gdr_slot_copy, n <= 16384.
+ */
+int gdr_slot_fork(const gdr_pool *pools, int n_pools, int slots, const int32_t *slot_table, const int32_t *parents,
+                  int n, int32_t *new_slot_table, gdr_stream_t stream);
+
+/*
+ * Closes the gaps: afterwards the slots in use are 0 .. n_live - 1.  The k-th live slot at or above n_live moves into the
+ * k-th free slot below it (both ascending); no other slot is touched, and the slots that were left keep their contents.
+ *   live      device int32 (slots): non-zero for a slot in use
+ *   new_slot  device int32 (slots): where slot s went (itself if it did not move), -1 for a free slot.  May not
+ *             overlap live
+ *   n_live    device int32 (1): the number of live slots
+ * Constraints: 1 <= n_pools <= GDR_MAX_POOLS, 1 <= slots <= 262144.
+ */
+int gdr_slot_compact(const gdr_pool *pools, int n_pools, int slots, const int32_t *live, int32_t *new_slot,
+                     int32_t *n_live, gdr_stream_t stream);
+
+/*
+ * Sets the slots idx[0 .. n) of every pool to zero bytes (the state a new sequence starts from) and marks them free.
+ *   idx    device int32 (n).  -1 is no slot; the same slot may be named twice
+ *   live   device int32 (slots) or NULL: live[idx[i]] = 0
+ * Another index outside [0, slots) is skipped and sets GDR_DEVERR_SLOT_INDEX.  Constraints: as for gdr_slot_copy.
+ */
+int gdr_slot_free(const gdr_pool *pools, int n_pools, int slots, const int32_t *idx, int n, int32_t *live,
+                  gdr_stream_t stream);
 
 /*
  * Stand-alone prologue (the same arithmetic the fused prologue applies), for
