@@ -29,33 +29,6 @@ __device__ __forceinline__ int seq_len(const int32_t *lengths, int b, int S) {
 }
 
 template <typename T, typename G, bool kMix>
-__global__ void __launch_bounds__(kThreads) scan_fwd_kernel(const ScanArgs a) {
-    const long long c = (long long)blockIdx.x * kThreads + threadIdx.x;
-    if (c >= (long long)a.B * a.N * a.D) return;
-    const int d = (int)(c % a.D);
-    const long long bn = c / a.D;
-    const int Lr = seq_len(a.lengths, (int)(bn / a.N), a.S);
-    if (Lr < 0) raise_device_error(a.err, GDR_DEVERR_LENGTH);
-    const int L = Lr < 0 ? 0 : Lr;
-    const T *x = static_cast<const T *>(a.x) + (size_t)bn * a.S * a.D + d;
-    const G *g = static_cast<const G *>(a.g) + (size_t)bn * a.S * a.D + d;
-    T *out = static_cast<T *>(a.out) + (size_t)bn * a.S * a.D + d;
-    float *ck = a.checkpoints ? a.checkpoints + (size_t)bn * ((a.S + kChunk - 1) / kChunk) * a.D + d : nullptr;
-    float h = a.initial_state ? a.initial_state[c] : 0.f;
-    for (int t = 0; t < a.S; ++t) {
-        const size_t at = (size_t)t * a.D;
-        if (ck && t % kChunk == 0 && (t < L || (t == 0 && Lr == 0))) ck[(size_t)(t / kChunk) * a.D] = h;
-        if (t < L) {
-            const float gt = to_f32(g[at]), at_ = expf(gt);
-            const float xt = to_f32(x[at]);
-            h = fmaf(at_, h, kMix ? one_minus_exp(gt, at_) * xt : xt);
-        }
-        out[at] = from_f32<T>(t < L ? h : 0.f);
-    }
-    if (a.final_state && Lr >= 0) a.final_state[c] = h;
-}
-
-template <typename T, typename G, bool kMix>
 __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(const ScanBwdArgs a) {
     const long long c = (long long)blockIdx.x * kThreads + threadIdx.x;
     if (c >= (long long)a.B * a.N * a.D) return;
@@ -147,12 +120,6 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(const ScanStepArgs 
     }
 }
 
-template <typename T, typename G, bool kMix> struct Fwd {
-    static void go(const ScanArgs &a, cudaStream_t s) {
-        const long long n = (long long)a.B * a.N * a.D;
-        scan_fwd_kernel<T, G, kMix><<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
-    }
-};
 template <typename T, typename G, bool kMix> struct Bwd {
     static void go(const ScanBwdArgs &a, cudaStream_t s) {
         const long long n = (long long)a.B * a.N * a.D;
@@ -182,9 +149,6 @@ cudaError_t dispatch(const Args &a, gdr_dtype dt, gdr_dtype gt, cudaStream_t s) 
 
 }  // namespace
 
-cudaError_t launch_scan_fwd(const ScanArgs &a, gdr_dtype dt, gdr_dtype gt, cudaStream_t s) {
-    return dispatch<Fwd>(a, dt, gt, s);
-}
 cudaError_t launch_scan_bwd(const ScanBwdArgs &a, gdr_dtype dt, gdr_dtype gt, cudaStream_t s) {
     return dispatch<Bwd>(a, dt, gt, s);
 }

@@ -1,0 +1,241 @@
+// scan_fwd.cu -- the gated linear recurrence over a sequence (gdr_scan_fwd): h_t = a_t h_{t-1} + b_t per channel, a_t =
+// exp(g_t), b_t = x_t or (1 - a_t) x_t.
+//
+// One pass over x and g (scan_tile.cuh).  The next tile's inputs are on their way (cp.async) while a tile is composed and
+// written.  Bound by HBM.
+#include "scan_tile.cuh"
+
+namespace gdr {
+namespace {
+using namespace scan;
+
+template <typename T, typename G, int V> struct Layout {
+    static constexpr int kCh = 32 * V;  // most channels of a tile
+    RawV<G, V> g[kSteps][kThreads];
+    RawV<T, V> x[kSteps][kThreads];
+    float wa[2][kWarps][kCh], wb[2][kWarps][kCh];        // (A, B) of every warp, for even and odd tiles
+    float ca[2][kMaxRanks][kCh], cb[2][kMaxRanks][kCh];  // (A, B) of every block of the cluster
+};
+
+template <typename T, typename G, bool kMix, int V>
+__global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a, const Cut cut) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    auto &sm = *reinterpret_cast<Layout<T, G, V> *>(smem);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int lx = cut.lx, cl = lane & (lx - 1);
+    const int seg = tid / lx;  // lanes of a segment are adjacent
+    const int R = cut.ranks, rank = (int)(blockIdx.x % R);
+    const long long unit = blockIdx.x / R;
+    const int slab = (int)(unit % cut.slabs);
+    const long long bn = unit / cut.slabs;
+    const int c0 = (slab * lx + cl) * V;
+    const bool on = c0 < a.D;
+    const int Lr = seq_len(a.lengths, (int)(bn / a.N), a.S);
+    const int L = Lr < 0 ? 0 : Lr;
+    if (Lr < 0 && tid == 0 && rank == 0) raise_device_error(a.err, GDR_DEVERR_LENGTH);
+
+    const size_t base = (size_t)bn * a.S * a.D + c0;
+    const T *x = static_cast<const T *>(a.x) + base;
+    const G *g = static_cast<const G *>(a.g) + base;
+    T *out = static_cast<T *>(a.out) + base;
+    float h[V];  // the state at the start of the cluster's next tiles, the same in every block
+#pragma unroll
+    for (int i = 0; i < V; ++i) h[i] = 0.f;
+    if (on && a.initial_state) load_f32<V>(a.initial_state + (size_t)bn * a.D + c0, h);
+    const int chunks = (a.S + kChunk - 1) / kChunk;
+    float *ck = a.checkpoints ? a.checkpoints + (size_t)bn * chunks * a.D + c0 : nullptr;
+    // an empty sequence makes no tile; its first checkpoint is its state
+    if (L == 0 && Lr == 0 && ck && on && seg == 0 && rank == 0 && a.S > 0) store<float, V>(ck, h);
+
+    const int TT = cut.tile();
+    const long long step = (long long)R * TT;  // tokens of the cluster's tiles
+    const int tiles = (int)((L + step - 1) / step);
+    if (R > 1 && tiles > 0) cluster_sync();  // every block of the cluster has started
+
+    auto fetch = [&](int k) {
+        const long long t0 = k * step + (long long)rank * TT + seg * kSteps;
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+            const bool in = on && t0 + j < L;
+            const size_t at = in ? (size_t)(t0 + j) * a.D : 0;
+            stage(&sm.g[j][tid], g + at, in);
+            stage(&sm.x[j][tid], x + at, in);
+        }
+        stage_commit();
+    };
+    if (tiles > 0) fetch(0);
+    for (int k = 0; k < tiles; ++k) {
+        const int p = k & 1;
+        const long long t0 = k * step + (long long)rank * TT + seg * kSteps;
+        // decays and writes of the segment (tokens behind the sequence: a = 1, b = 0), and the segment as a whole
+        float av[kSteps][V], bv[kSteps][V], A[V], B[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            A[i] = 1.f;
+            B[i] = 0.f;
+        }
+        stage_wait();
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+            float gv[V];
+            unpack<G, V>(sm.g[j][tid], gv);
+            unpack<T, V>(sm.x[j][tid], bv[j]);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                av[j][i] = expf(gv[i]);
+                if (kMix) bv[j][i] *= one_minus_exp(gv[i], av[j][i]);
+                A[i] *= av[j][i];
+                B[i] = fmaf(av[j][i], B[i], bv[j][i]);
+            }
+        }
+        // inclusive composition over the segments of the warp; (EA, EB): the segments before this one
+        float EA[V], EB[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            EA[i] = 1.f;
+            EB[i] = 0.f;
+        }
+        if (lx < 32) {
+            for (int d = lx; d < 32; d *= 2) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float pa = __shfl_up_sync(0xffffffffu, A[i], d), pb = __shfl_up_sync(0xffffffffu, B[i], d);
+                    if (lane >= d) {
+                        B[i] = fmaf(A[i], pb, B[i]);
+                        A[i] *= pa;
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float pa = __shfl_up_sync(0xffffffffu, A[i], lx), pb = __shfl_up_sync(0xffffffffu, B[i], lx);
+                if (lane >= lx) {
+                    EA[i] = pa;
+                    EB[i] = pb;
+                }
+            }
+        }
+        if (lane >= 32 - lx) {  // the warp's last segment holds the whole warp
+            store<float, V>(&sm.wa[p][warp][cl * V], A);
+            store<float, V>(&sm.wb[p][warp][cl * V], B);
+        }
+        __syncthreads();
+        if (k + 1 < tiles) fetch(k + 1);  // every thread has taken its own inputs out of the stage
+        if (R > 1) {
+            if (tid < lx) {  // the block as a whole, to every block of the cluster
+                float ta[V], tb[V];
+                load_f32<V>(&sm.wa[p][0][cl * V], ta);
+                load_f32<V>(&sm.wb[p][0][cl * V], tb);
+                for (int w = 1; w < kWarps; ++w) {
+                    float wa[V], wb[V];
+                    load_f32<V>(&sm.wa[p][w][cl * V], wa);
+                    load_f32<V>(&sm.wb[p][w][cl * V], wb);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        tb[i] = fmaf(wa[i], tb[i], wb[i]);
+                        ta[i] *= wa[i];
+                    }
+                }
+                for (int r = 0; r < R; ++r) {
+                    put_remote<V>(&sm.ca[p][rank][cl * V], r, ta);
+                    put_remote<V>(&sm.cb[p][rank][cl * V], r, tb);
+                }
+            }
+            cluster_sync();
+        }
+        // the state this thread starts from: the tile's start, the blocks and warps before it, its warp's segments
+        float hs[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) hs[i] = h[i];
+        for (int r = 0; r < (R > 1 ? R : 0); ++r) {
+            float ra[V], rb[V];
+            load_f32<V>(&sm.ca[p][r][cl * V], ra);
+            load_f32<V>(&sm.cb[p][r][cl * V], rb);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                h[i] = fmaf(ra[i], h[i], rb[i]);
+                if (r < rank) hs[i] = h[i];
+            }
+        }
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (R > 1 && w >= warp) break;
+            float wa[V], wb[V];
+            load_f32<V>(&sm.wa[p][w][cl * V], wa);
+            load_f32<V>(&sm.wb[p][w][cl * V], wb);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (R > 1) {
+                    hs[i] = fmaf(wa[i], hs[i], wb[i]);
+                } else {
+                    h[i] = fmaf(wa[i], h[i], wb[i]);
+                    if (w < warp) hs[i] = h[i];
+                }
+            }
+        }
+        if (lx < 32) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) hs[i] = fmaf(EA[i], hs[i], EB[i]);
+        }
+        if (on && t0 < a.S) {
+            // segments are kSteps long and tiles a multiple of 64: a chunk starts where a segment does
+            if (ck && (t0 & (kChunk - 1)) == 0 && t0 < L) store<float, V>(ck + (size_t)(t0 / kChunk) * a.D, hs);
+            T *o = out + (size_t)t0 * a.D;
+            const int n = (int)min((long long)kSteps, a.S - t0), nv = (int)max(0LL, min((long long)kSteps, L - t0));
+#pragma unroll
+            for (int j = 0; j < kSteps; ++j) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) hs[i] = j < nv ? fmaf(av[j][i], hs[i], bv[j][i]) : 0.f;
+                if (j < n) store<T, V>(o + (size_t)j * a.D, hs);
+            }
+        }
+    }
+    if (!on) return;
+    // tokens behind the last tile
+    float zero[V] = {};
+    for (long long t = tiles * step + (long long)rank * (kThreads / lx) + seg; t < a.S; t += (long long)R * (kThreads / lx))
+        store<T, V>(out + (size_t)t * a.D, zero);
+    if (a.final_state && Lr >= 0 && seg == 0 && rank == 0) store<float, V>(a.final_state + (size_t)bn * a.D + c0, h);
+}
+
+template <typename T, typename G, bool kMix, int V> cudaError_t launch_v(const ScanArgs &a, cudaStream_t s) {
+    static LaunchCache cache(reinterpret_cast<const void *>(scan_fwd_kernel<T, G, kMix, V>));
+    const int smem = (int)sizeof(Layout<T, G, V>);
+    int grid = 0;
+    cudaError_t e = cache.allow_smem(smem);
+    if (e == cudaSuccess) e = cache.resident_grid(kThreads, smem, &grid);  // two blocks an SM
+    if (e != cudaSuccess) return e;
+    const Cut cut = choose_cut((long long)a.B * a.N, a.D, V, a.S, 32, grid / 2);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((long long)a.B * a.N * cut.slabs * cut.ranks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = cut.ranks;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = cut.ranks > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, scan_fwd_kernel<T, G, kMix, V>, a, cut);
+}
+
+// vectors of 4 channels where rows are made of whole ones, of 2, else single channels
+template <typename T, typename G, bool kMix> cudaError_t launch_m(const ScanArgs &a, cudaStream_t s) {
+    if (a.D % 4 == 0) return launch_v<T, G, kMix, 4>(a, s);
+    if (a.D % 2 == 0) return launch_v<T, G, kMix, 2>(a, s);
+    return launch_v<T, G, kMix, 1>(a, s);
+}
+template <typename T, typename G> cudaError_t launch_t(const ScanArgs &a, cudaStream_t s) {
+    return a.mode == GDR_SCAN_MIX ? launch_m<T, G, true>(a, s) : launch_m<T, G, false>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_scan_fwd(const ScanArgs &a, gdr_dtype dt, gdr_dtype gt, cudaStream_t s) {
+    if (dt == GDR_F32) return launch_t<float, float>(a, s);
+    if (dt == GDR_BF16) return gt == dt ? launch_t<__nv_bfloat16, __nv_bfloat16>(a, s) : launch_t<__nv_bfloat16, float>(a, s);
+    return gt == dt ? launch_t<__half, __half>(a, s) : launch_t<__half, float>(a, s);
+}
+
+}  // namespace gdr
