@@ -444,6 +444,7 @@ int check_scan(int B, int N, int S, int D, int dtype, int gate_dtype, int mode) 
     if (gate_dtype != GDR_F32 && gate_dtype != dtype) return GDR_ERR_DTYPE;
     if (mode != GDR_SCAN_ADD && mode != GDR_SCAN_MIX) return GDR_ERR_SHAPE;
     if (B < 0 || S < 0 || N < 1 || D < 1) return GDR_ERR_SHAPE;
+    if (D > 1 << 26) return GDR_ERR_SHAPE;  // the kernels keep a row's bytes in 32 bits
     // channels are counted in 31 bits (grids, channel indices); offsets into the tensors are 64-bit
     if ((long long)B * N >= (1LL << 31) || (long long)B * N * D >= (1LL << 31)) return GDR_ERR_SHAPE;
     if ((long long)N * D >= (1LL << 31) || (double)B * N * D * S >= 0x1p60) return GDR_ERR_SHAPE;
@@ -474,7 +475,7 @@ extern "C" int gdr_scan_fwd(const void *x, const void *g, const float *initial_s
     ScanArgs a{};
     a.x = x; a.g = g; a.initial_state = initial_state; a.lengths = actual_seq_lengths;
     a.B = B; a.N = N; a.S = S; a.D = D; a.mode = mode;
-    a.out = out; a.final_state = final_state; a.checkpoints = checkpoints; a.err = err;
+    a.out = out; a.final_state = final_state; a.checkpoints = checkpoints; a.err = err; a.wait_ns = chunk_wait_ns();
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     if (checks_enabled() && (st = check_lengths_host(actual_seq_lengths, B, S, cs))) return st;
     return launch_scan_fwd(a, dtype, gate_dtype, cs) == cudaSuccess ? GDR_OK : GDR_ERR_LAUNCH;
@@ -504,7 +505,7 @@ extern "C" int gdr_scan_bwd(const void *x, const void *g, const float *checkpoin
     a.x = x; a.g = g; a.checkpoints = checkpoints; a.dout = dout; a.dfinal_state = dfinal_state;
     a.lengths = actual_seq_lengths;
     a.B = B; a.N = N; a.S = S; a.D = D; a.mode = mode;
-    a.dx = dx; a.dg = dg; a.dinitial_state = dinitial_state; a.err = err;
+    a.dx = dx; a.dg = dg; a.dinitial_state = dinitial_state; a.err = err; a.wait_ns = chunk_wait_ns();
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     if (checks_enabled() && (st = check_lengths_host(actual_seq_lengths, B, S, cs))) return st;
     return launch_scan_bwd(a, dtype, gate_dtype, cs) == cudaSuccess ? GDR_OK : GDR_ERR_LAUNCH;

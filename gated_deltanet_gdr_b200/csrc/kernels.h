@@ -130,6 +130,7 @@ struct ScanArgs {
     void *out;
     float *final_state, *checkpoints;
     unsigned int *err;
+    uint64_t wait_ns;  // limit of each wait for another block of the cluster
 };
 struct ScanBwdArgs {
     const void *x, *g;
@@ -141,6 +142,7 @@ struct ScanBwdArgs {
     void *dx, *dg;
     float *dinitial_state;
     unsigned int *err;
+    uint64_t wait_ns;
 };
 struct ScanStepArgs {
     const void *x, *g;

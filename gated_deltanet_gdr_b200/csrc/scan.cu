@@ -29,50 +29,6 @@ __device__ __forceinline__ int seq_len(const int32_t *lengths, int b, int S) {
 }
 
 template <typename T, typename G, bool kMix>
-__global__ void __launch_bounds__(kThreads) scan_bwd_kernel(const ScanBwdArgs a) {
-    const long long c = (long long)blockIdx.x * kThreads + threadIdx.x;
-    if (c >= (long long)a.B * a.N * a.D) return;
-    const int d = (int)(c % a.D);
-    const long long bn = c / a.D;
-    const int Lr = seq_len(a.lengths, (int)(bn / a.N), a.S);
-    if (Lr < 0) raise_device_error(a.err, GDR_DEVERR_LENGTH);
-    const int L = Lr < 0 ? 0 : Lr;
-    const size_t base = (size_t)bn * a.S * a.D + d;
-    const T *x = static_cast<const T *>(a.x) + base, *dout = static_cast<const T *>(a.dout) + base;
-    const G *g = static_cast<const G *>(a.g) + base;
-    T *dx = static_cast<T *>(a.dx) + base;
-    G *dg = static_cast<G *>(a.dg) + base;
-    const int chunks = (a.S + kChunk - 1) / kChunk;
-    const float *ck = a.checkpoints + (size_t)bn * chunks * a.D + d;
-    float mu = Lr >= 0 && a.dfinal_state ? a.dfinal_state[c] : 0.f;
-    float before[kChunk];
-    for (int k = chunks - 1; k >= 0; --k) {
-        const int t0 = k * kChunk, t1 = min(t0 + kChunk, a.S), tv = min(t1, L);
-        float h = t0 < tv ? ck[(size_t)k * a.D] : 0.f;
-        for (int t = t0; t < tv; ++t) {
-            const size_t at = (size_t)t * a.D;
-            before[t - t0] = h;
-            const float gt = to_f32(g[at]), at_ = expf(gt), xt = to_f32(x[at]);
-            h = fmaf(at_, h, kMix ? one_minus_exp(gt, at_) * xt : xt);
-        }
-        for (int t = t1 - 1; t >= t0; --t) {
-            const size_t at = (size_t)t * a.D;
-            float rx = 0.f, rg = 0.f;
-            if (t < tv) {
-                const float gt = to_f32(g[at]), at_ = expf(gt), xt = to_f32(x[at]);
-                const float lam = to_f32(dout[at]) + mu;
-                mu = at_ * lam;
-                rx = kMix ? one_minus_exp(gt, at_) * lam : lam;
-                rg = mu * (kMix ? before[t - t0] - xt : before[t - t0]);
-            }
-            dx[at] = from_f32<T>(rx);
-            dg[at] = from_f32<G>(rg);
-        }
-    }
-    if (a.dinitial_state) a.dinitial_state[c] = mu;
-}
-
-template <typename T, typename G, bool kMix>
 __global__ void __launch_bounds__(kThreads) scan_step_kernel(const ScanStepArgs a) {
     const long long c = (long long)blockIdx.x * kThreads + threadIdx.x;
     const long long per = (long long)a.N * a.D;
@@ -120,12 +76,6 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(const ScanStepArgs 
     }
 }
 
-template <typename T, typename G, bool kMix> struct Bwd {
-    static void go(const ScanBwdArgs &a, cudaStream_t s) {
-        const long long n = (long long)a.B * a.N * a.D;
-        scan_bwd_kernel<T, G, kMix><<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
-    }
-};
 template <typename T, typename G, bool kMix> struct Step {
     static void go(const ScanStepArgs &a, cudaStream_t s) {
         const long long n = (long long)a.B * a.N * a.D;
@@ -149,9 +99,6 @@ cudaError_t dispatch(const Args &a, gdr_dtype dt, gdr_dtype gt, cudaStream_t s) 
 
 }  // namespace
 
-cudaError_t launch_scan_bwd(const ScanBwdArgs &a, gdr_dtype dt, gdr_dtype gt, cudaStream_t s) {
-    return dispatch<Bwd>(a, dt, gt, s);
-}
 cudaError_t launch_scan_step(const ScanStepArgs &a, gdr_dtype dt, gdr_dtype gt, cudaStream_t s) {
     return dispatch<Step>(a, dt, gt, s);
 }

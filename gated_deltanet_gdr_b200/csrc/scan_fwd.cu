@@ -9,12 +9,15 @@ namespace gdr {
 namespace {
 using namespace scan;
 
+constexpr int kSteps = 8;  // tokens of a thread in a tile
+
 template <typename T, typename G, int V> struct Layout {
     static constexpr int kCh = 32 * V;  // most channels of a tile
     RawV<G, V> g[kSteps][kThreads];
     RawV<T, V> x[kSteps][kThreads];
     float wa[2][kWarps][kCh], wb[2][kWarps][kCh];        // (A, B) of every warp, for even and odd tiles
     float ca[2][kMaxRanks][kCh], cb[2][kMaxRanks][kCh];  // (A, B) of every block of the cluster
+    uint64_t arrived[2];                                 // their bytes
 };
 
 template <typename T, typename G, bool kMix, int V>
@@ -34,33 +37,40 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
     const int L = Lr < 0 ? 0 : Lr;
     if (Lr < 0 && tid == 0 && rank == 0) raise_device_error(a.err, GDR_DEVERR_LENGTH);
 
+    constexpr int P = kPairs<V>;
+    const unsigned row_x = (unsigned)a.D * sizeof(T), row_g = (unsigned)a.D * sizeof(G);  // D <= 2^26
     const size_t base = (size_t)bn * a.S * a.D + c0;
-    const T *x = static_cast<const T *>(a.x) + base;
-    const G *g = static_cast<const G *>(a.g) + base;
-    T *out = static_cast<T *>(a.out) + base;
-    float h[V];  // the state at the start of the cluster's next tiles, the same in every block
-#pragma unroll
-    for (int i = 0; i < V; ++i) h[i] = 0.f;
+    const char *x = reinterpret_cast<const char *>(static_cast<const T *>(a.x) + base);
+    const char *g = reinterpret_cast<const char *>(static_cast<const G *>(a.g) + base);
+    char *out = reinterpret_cast<char *>(static_cast<T *>(a.out) + base);
+    f2_t h[P];  // the state at the start of the cluster's next tiles, the same in every block
+    fill(h, 0.f);
     if (on && a.initial_state) load_f32<V>(a.initial_state + (size_t)bn * a.D + c0, h);
     const int chunks = (a.S + kChunk - 1) / kChunk;
     float *ck = a.checkpoints ? a.checkpoints + (size_t)bn * chunks * a.D + c0 : nullptr;
     // an empty sequence makes no tile; its first checkpoint is its state
     if (L == 0 && Lr == 0 && ck && on && seg == 0 && rank == 0 && a.S > 0) store<float, V>(ck, h);
 
-    const int TT = cut.tile();
+    const int TT = kSteps * (kThreads / lx);
     const long long step = (long long)R * TT;  // tokens of the cluster's tiles
     const int tiles = (int)((L + step - 1) / step);
-    if (R > 1 && tiles > 0) cluster_sync();  // every block of the cluster has started
+    const unsigned exchange = (unsigned)(R * lx * V * 2 * sizeof(float));  // bytes of a tile's (A, B) of all blocks
+    bool lost = false;  // a wait ran out: no further waits
+    if (R > 1) {
+        if (tid == 0) {
+            sm100::mbar_init(&sm.arrived[0], 1);
+            sm100::mbar_init(&sm.arrived[1], 1);
+            sm100::fence_mbar_init();
+        }
+        cluster_meet();  // every block of the cluster has started, with its barriers ready
+    }
 
     auto fetch = [&](int k) {
         const long long t0 = k * step + (long long)rank * TT + seg * kSteps;
-#pragma unroll
-        for (int j = 0; j < kSteps; ++j) {
-            const bool in = on && t0 + j < L;
-            const size_t at = in ? (size_t)(t0 + j) * a.D : 0;
-            stage(&sm.g[j][tid], g + at, in);
-            stage(&sm.x[j][tid], x + at, in);
-        }
+        const int n = on ? (int)max(0LL, min((long long)kSteps, L - t0)) : 0;
+        const size_t at = n > 0 ? (size_t)t0 : 0;
+        stage_segment<kSteps>(sm.g, g + at * row_g, row_g, n);
+        stage_segment<kSteps>(sm.x, x + at * row_x, row_x, n);
         stage_commit();
     };
     if (tiles > 0) fetch(0);
@@ -68,47 +78,40 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
         const int p = k & 1;
         const long long t0 = k * step + (long long)rank * TT + seg * kSteps;
         // decays and writes of the segment (tokens behind the sequence: a = 1, b = 0), and the segment as a whole
-        float av[kSteps][V], bv[kSteps][V], A[V], B[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            A[i] = 1.f;
-            B[i] = 0.f;
-        }
+        f2_t av[kSteps][P], bv[kSteps][P], A[P], B[P];
         stage_wait();
 #pragma unroll
         for (int j = 0; j < kSteps; ++j) {
-            float gv[V];
+            f2_t gv[P];
             unpack<G, V>(sm.g[j][tid], gv);
             unpack<T, V>(sm.x[j][tid], bv[j]);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                av[j][i] = expf(gv[i]);
-                if (kMix) bv[j][i] *= one_minus_exp(gv[i], av[j][i]);
-                A[i] *= av[j][i];
-                B[i] = fmaf(av[j][i], B[i], bv[j][i]);
+            for (int i = 0; i < P; ++i) {
+                f2_t rest;
+                decay<kMix>(gv[i], av[j][i], rest);
+                if (kMix) bv[j][i] = mul2(bv[j][i], rest);
+                A[i] = j ? mul2(A[i], av[j][i]) : av[j][i];
+                B[i] = j ? fma2(av[j][i], B[i], bv[j][i]) : bv[j][i];
             }
         }
         // inclusive composition over the segments of the warp; (EA, EB): the segments before this one
-        float EA[V], EB[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            EA[i] = 1.f;
-            EB[i] = 0.f;
-        }
+        f2_t EA[P], EB[P];
+        fill(EA, 1.f);
+        fill(EB, 0.f);
         if (lx < 32) {
             for (int d = lx; d < 32; d *= 2) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float pa = __shfl_up_sync(0xffffffffu, A[i], d), pb = __shfl_up_sync(0xffffffffu, B[i], d);
+                for (int i = 0; i < P; ++i) {
+                    const f2_t pa = shfl_up2(A[i], d), pb = shfl_up2(B[i], d);
                     if (lane >= d) {
-                        B[i] = fmaf(A[i], pb, B[i]);
-                        A[i] *= pa;
+                        B[i] = fma2(A[i], pb, B[i]);
+                        A[i] = mul2(A[i], pa);
                     }
                 }
             }
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float pa = __shfl_up_sync(0xffffffffu, A[i], lx), pb = __shfl_up_sync(0xffffffffu, B[i], lx);
+            for (int i = 0; i < P; ++i) {
+                const f2_t pa = shfl_up2(A[i], lx), pb = shfl_up2(B[i], lx);
                 if (lane >= lx) {
                     EA[i] = pa;
                     EB[i] = pb;
@@ -122,79 +125,96 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
         __syncthreads();
         if (k + 1 < tiles) fetch(k + 1);  // every thread has taken its own inputs out of the stage
         if (R > 1) {
-            if (tid < lx) {  // the block as a whole, to every block of the cluster
-                float ta[V], tb[V];
+            // the block as a whole to every block of the cluster, one warp for each.  A block writes a place again two
+            // tiles on, having received the tile between, which its owner sent after reading this one.
+            if (tid == 0) sm100::mbar_arrive_expect_tx(&sm.arrived[p], exchange);
+            if (warp < R && lane < lx) {
+                f2_t ta[P], tb[P];
                 load_f32<V>(&sm.wa[p][0][cl * V], ta);
                 load_f32<V>(&sm.wb[p][0][cl * V], tb);
+#pragma unroll
                 for (int w = 1; w < kWarps; ++w) {
-                    float wa[V], wb[V];
+                    f2_t wa[P], wb[P];
                     load_f32<V>(&sm.wa[p][w][cl * V], wa);
                     load_f32<V>(&sm.wb[p][w][cl * V], wb);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        tb[i] = fmaf(wa[i], tb[i], wb[i]);
-                        ta[i] *= wa[i];
+                    for (int i = 0; i < P; ++i) {
+                        tb[i] = fma2(wa[i], tb[i], wb[i]);
+                        ta[i] = mul2(ta[i], wa[i]);
                     }
                 }
-                for (int r = 0; r < R; ++r) {
-                    put_remote<V>(&sm.ca[p][rank][cl * V], r, ta);
-                    put_remote<V>(&sm.cb[p][rank][cl * V], r, tb);
-                }
+                put_remote<V>(&sm.ca[p][rank][cl * V], &sm.arrived[p], warp, ta);
+                put_remote<V>(&sm.cb[p][rank][cl * V], &sm.arrived[p], warp, tb);
             }
-            cluster_sync();
+            __syncwarp();
+            if (!lost && !wait_remote(&sm.arrived[p], (unsigned)(k >> 1) & 1u, a.wait_ns)) {
+                lost = true;
+                raise_device_error(a.err, GDR_DEVERR_TIMEOUT);
+            }
         }
         // the state this thread starts from: the tile's start, the blocks and warps before it, its warp's segments
-        float hs[V];
+        f2_t hs[P];
 #pragma unroll
-        for (int i = 0; i < V; ++i) hs[i] = h[i];
+        for (int i = 0; i < P; ++i) hs[i] = h[i];
         for (int r = 0; r < (R > 1 ? R : 0); ++r) {
-            float ra[V], rb[V];
+            f2_t ra[P], rb[P];
             load_f32<V>(&sm.ca[p][r][cl * V], ra);
             load_f32<V>(&sm.cb[p][r][cl * V], rb);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                h[i] = fmaf(ra[i], h[i], rb[i]);
+            for (int i = 0; i < P; ++i) {
+                h[i] = fma2(ra[i], h[i], rb[i]);
                 if (r < rank) hs[i] = h[i];
             }
         }
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             if (R > 1 && w >= warp) break;
-            float wa[V], wb[V];
+            f2_t wa[P], wb[P];
             load_f32<V>(&sm.wa[p][w][cl * V], wa);
             load_f32<V>(&sm.wb[p][w][cl * V], wb);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
+            for (int i = 0; i < P; ++i) {
                 if (R > 1) {
-                    hs[i] = fmaf(wa[i], hs[i], wb[i]);
+                    hs[i] = fma2(wa[i], hs[i], wb[i]);
                 } else {
-                    h[i] = fmaf(wa[i], h[i], wb[i]);
+                    h[i] = fma2(wa[i], h[i], wb[i]);
                     if (w < warp) hs[i] = h[i];
                 }
             }
         }
         if (lx < 32) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) hs[i] = fmaf(EA[i], hs[i], EB[i]);
+            for (int i = 0; i < P; ++i) hs[i] = fma2(EA[i], hs[i], EB[i]);
         }
         if (on && t0 < a.S) {
             // segments are kSteps long and tiles a multiple of 64: a chunk starts where a segment does
             if (ck && (t0 & (kChunk - 1)) == 0 && t0 < L) store<float, V>(ck + (size_t)(t0 / kChunk) * a.D, hs);
-            T *o = out + (size_t)t0 * a.D;
-            const int n = (int)min((long long)kSteps, a.S - t0), nv = (int)max(0LL, min((long long)kSteps, L - t0));
+            char *o = out + (size_t)t0 * row_x;
+            if (t0 + kSteps <= L) {
 #pragma unroll
-            for (int j = 0; j < kSteps; ++j) {
+                for (int j = 0; j < kSteps; ++j) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) hs[i] = j < nv ? fmaf(av[j][i], hs[i], bv[j][i]) : 0.f;
-                if (j < n) store<T, V>(o + (size_t)j * a.D, hs);
+                    for (int i = 0; i < P; ++i) hs[i] = fma2(av[j][i], hs[i], bv[j][i]);
+                    store<T, V>(o + j * (size_t)row_x, hs);
+                }
+            } else {
+                const int n = (int)min((long long)kSteps, a.S - t0), nv = (int)max(0LL, L - t0);
+#pragma unroll
+                for (int j = 0; j < kSteps; ++j) {
+#pragma unroll
+                    for (int i = 0; i < P; ++i) hs[i] = j < nv ? fma2(av[j][i], hs[i], bv[j][i]) : 0;
+                    if (j < n) store<T, V>(o + j * (size_t)row_x, hs);
+                }
             }
         }
     }
+    if (R > 1) cluster_meet();  // a block that gave up must not leave while the others write to it
     if (!on) return;
     // tokens behind the last tile
-    float zero[V] = {};
+    f2_t zero[P];
+    fill(zero, 0.f);
     for (long long t = tiles * step + (long long)rank * (kThreads / lx) + seg; t < a.S; t += (long long)R * (kThreads / lx))
-        store<T, V>(out + (size_t)t * a.D, zero);
+        store<T, V>(out + (size_t)t * row_x, zero);
     if (a.final_state && Lr >= 0 && seg == 0 && rank == 0) store<float, V>(a.final_state + (size_t)bn * a.D + c0, h);
 }
 
@@ -205,7 +225,7 @@ template <typename T, typename G, bool kMix, int V> cudaError_t launch_v(const S
     cudaError_t e = cache.allow_smem(smem);
     if (e == cudaSuccess) e = cache.resident_grid(kThreads, smem, &grid);  // two blocks an SM
     if (e != cudaSuccess) return e;
-    const Cut cut = choose_cut((long long)a.B * a.N, a.D, V, a.S, 32, grid / 2);
+    const Cut cut = choose_cut((long long)a.B * a.N, a.D, V, a.S, kSteps, 32, 4, grid / 2);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((long long)a.B * a.N * cut.slabs * cut.ranks));
     cfg.blockDim = dim3(kThreads);

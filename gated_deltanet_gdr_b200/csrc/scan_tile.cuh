@@ -13,25 +13,67 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "sm100.cuh"
 
 namespace gdr {
 namespace scan {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kSteps = 8;     // tokens of a thread in a tile
 constexpr int kMaxRanks = 8;  // blocks of a cluster (the portable limit)
 
-// 1 - e^g without cancellation: the Taylor series -g (1 + g/2 (1 + g/3 (...))) near 0, where its first dropped term is
-// below 2^-24 of the sum, and the difference elsewhere (e^g <= 0.78 there, so it loses under three bits)
-__device__ __forceinline__ float one_minus_exp(float g, float a) {
-    float p = fmaf(g, 1.f / 7.f, 1.f);
-    p = fmaf(g * (1.f / 6.f), p, 1.f);
-    p = fmaf(g * (1.f / 5.f), p, 1.f);
-    p = fmaf(g * (1.f / 4.f), p, 1.f);
-    p = fmaf(g * (1.f / 3.f), p, 1.f);
-    p = fmaf(g * (1.f / 2.f), p, 1.f);
-    return fabsf(g) >= 0.25f ? 1.f - a : -g * p;
+// ---- channels in pairs (f32x2 arithmetic) ------------------------------------------------------------------------
+
+template <int V> constexpr int kPairs = (V + 1) / 2;  // a single channel fills half of one
+
+__device__ __forceinline__ f2_t add2(f2_t a, f2_t b) {
+    f2_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f2_t both(float x) { return pk2(x, x); }
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// a = e^g, and (kRest) rest = 1 - e^g, of a pair.  Near 0 the Taylor series, whose first dropped term is below a tenth
+// of a rounding (2^-24) of a for |g| < 1/8, or below one rounding of the rest for |g| < 1/4: the rest keeps its digits, and
+// a decay close to 1 is good to a rounding -- it is applied hundreds of times, and what ex2.approx loses (up to 2^-22)
+// would add up.  Elsewhere ex2(g log2 e), whose argument is rounded once more (|g| 2^-24): there a state fades soon.
+template <bool kRest> __device__ __forceinline__ void decay(f2_t g, f2_t &a, f2_t &rest) {
+    f2_t near_a, near_rest = 0;
+    if (kRest) {  // -g (1 + g/2 + ... + g^5/720)
+        f2_t p = both(-1.f / 720.f);
+        p = fma2(p, g, both(-1.f / 120.f));
+        p = fma2(p, g, both(-1.f / 24.f));
+        p = fma2(p, g, both(-1.f / 6.f));
+        p = fma2(p, g, both(-0.5f));
+        p = fma2(p, g, both(-1.f));
+        near_rest = mul2(p, g);
+        near_a = fma2(near_rest, both(-1.f), both(1.f));
+    } else {  // 1 + g + ... + g^5/120
+        f2_t p = both(1.f / 120.f);
+        p = fma2(p, g, both(1.f / 24.f));
+        p = fma2(p, g, both(1.f / 6.f));
+        p = fma2(p, g, both(0.5f));
+        p = fma2(p, g, both(1.f));
+        near_a = fma2(p, g, both(1.f));
+    }
+    const f2_t t = mul2(g, both(1.4426950408889634f));
+    constexpr float kNear = kRest ? 0.25f : 0.125f;
+    float g0, g1, t0, t1, n0, n1, r0, r1;
+    up2(g, g0, g1);
+    up2(t, t0, t1);
+    up2(near_a, n0, n1);
+    const bool s0 = fabsf(g0) < kNear, s1 = fabsf(g1) < kNear;
+    const float f0 = ex2(t0), f1 = ex2(t1);
+    a = pk2(s0 ? n0 : f0, s1 ? n1 : f1);
+    if (kRest) {
+        up2(near_rest, r0, r1);
+        rest = pk2(s0 ? r0 : 1.f - f0, s1 ? r1 : 1.f - f1);
+    }
 }
 
 // length of sequence b, or -1 for one outside [0, S]
@@ -49,36 +91,76 @@ template <> struct Raw<8> { using type = uint2; };
 template <> struct Raw<16> { using type = uint4; };
 template <typename T, int V> using RawV = typename Raw<(int)sizeof(T) * V>::type;
 
-template <typename T, int V> __device__ __forceinline__ void unpack(const RawV<T, V> &r, float (&x)[V]) {
+
+template <typename T, int V> __device__ __forceinline__ void unpack(const RawV<T, V> &r, f2_t (&x)[kPairs<V>]) {
     const T *e = reinterpret_cast<const T *>(&r);
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = to_f32(e[i]);
+    for (int i = 0; i < kPairs<V>; ++i) x[i] = pk2(to_f32(e[2 * i]), 2 * i + 1 < V ? to_f32(e[2 * i + 1 < V ? 2 * i + 1 : 0]) : 0.f);
 }
-template <typename T, int V> __device__ __forceinline__ void store(T *p, const float (&x)[V]) {
+template <typename T, int V> __device__ __forceinline__ void store(void *p, const f2_t (&x)[kPairs<V>]) {
     RawV<T, V> r;
     T *e = reinterpret_cast<T *>(&r);
 #pragma unroll
-    for (int i = 0; i < V; ++i) e[i] = from_f32<T>(x[i]);
-    *reinterpret_cast<RawV<T, V> *>(p) = r;
+    for (int i = 0; i < kPairs<V>; ++i) {
+        float lo, hi;
+        up2(x[i], lo, hi);
+        e[2 * i] = from_f32<T>(lo);
+        if (2 * i + 1 < V) e[2 * i + 1 < V ? 2 * i + 1 : 0] = from_f32<T>(hi);
+    }
+    *static_cast<RawV<T, V> *>(p) = r;
 }
-template <int V> __device__ __forceinline__ void load_f32(const float *p, float (&x)[V]) {
+template <int V> __device__ __forceinline__ void load_f32(const float *p, f2_t (&x)[kPairs<V>]) {
     unpack<float, V>(*reinterpret_cast<const RawV<float, V> *>(p), x);
+}
+template <int P> __device__ __forceinline__ void fill(f2_t (&x)[P], float v) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) x[i] = both(v);
+}
+// pair x from the lane `d` below (or above: the shuffles of a pair are two)
+__device__ __forceinline__ f2_t shfl_up2(f2_t x, int d) {
+    float lo, hi;
+    up2(x, lo, hi);
+    return pk2(__shfl_up_sync(0xffffffffu, lo, d), __shfl_up_sync(0xffffffffu, hi, d));
+}
+__device__ __forceinline__ f2_t shfl_down2(f2_t x, int d) {
+    float lo, hi;
+    up2(x, lo, hi);
+    return pk2(__shfl_down_sync(0xffffffffu, lo, d), __shfl_down_sync(0xffffffffu, hi, d));
 }
 
 // ---- staging: every thread copies its own inputs to a place of its own, so that no barrier is needed to read them --
 
 // copies one element vector to shared memory, or zeros where !on (src is then not read)
-template <typename R> __device__ __forceinline__ void stage(R *dst, const void *src, bool on) {
+template <typename R, bool kMask> __device__ __forceinline__ void stage(R *dst, const void *src, bool on) {
     if constexpr (sizeof(R) >= 4) {
         const unsigned d = (unsigned)__cvta_generic_to_shared(dst);
-        const int n = on ? (int)sizeof(R) : 0;
-        if constexpr (sizeof(R) == 16)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
-        else
-            asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(sizeof(R)), "r"(n)
-                         : "memory");
+        if constexpr (!kMask) {
+            if constexpr (sizeof(R) == 16)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+            else
+                asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(sizeof(R)) : "memory");
+        } else {
+            const int n = on ? (int)sizeof(R) : 0;
+            if constexpr (sizeof(R) == 16)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
+            else
+                asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(sizeof(R)), "r"(n)
+                             : "memory");
+        }
     } else {
-        *dst = on ? *static_cast<const R *>(src) : R{};
+        *dst = !kMask || on ? *static_cast<const R *>(src) : R{};
+    }
+}
+// a thread's TS tokens of one tensor, rows `row` bytes apart, n of them valid (the others zero); src is the first
+template <int TS, typename R>
+__device__ __forceinline__ void stage_segment(R (*dst)[kThreads], const void *src, unsigned row, int n) {
+    const char *p = static_cast<const char *>(src);
+    if (n == TS) {
+#pragma unroll
+        for (int j = 0; j < TS; ++j) stage<R, false>(&dst[j][threadIdx.x], p + j * (size_t)row, true);
+    } else {
+#pragma unroll
+        for (int j = 0; j < TS; ++j) stage<R, true>(&dst[j][threadIdx.x], j < n ? p + j * (size_t)row : p, j < n);
     }
 }
 __device__ __forceinline__ void stage_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -86,21 +168,56 @@ __device__ __forceinline__ void stage_wait() { asm volatile("cp.async.wait_group
 
 // ---- clusters -----------------------------------------------------------------------------------------------------
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+// every thread of every block of the cluster passes together; orders no memory but mbarrier initialisations fenced before
+__device__ __forceinline__ void cluster_meet() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
-// writes V floats at `p` (an address in this block's shared memory) in block `rank` of the cluster
-template <int V> __device__ __forceinline__ void put_remote(float *p, int rank, const float (&x)[V]) {
-    const unsigned local = (unsigned)__cvta_generic_to_shared(p);
-    unsigned a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(local), "r"(rank));
+// writes V floats at `p` and their bytes to the count of `bar` (both given as this block's addresses) in block `rank`
+template <int V> __device__ __forceinline__ void put_remote(const float *p, const uint64_t *bar, int rank, const f2_t (&v)[kPairs<V>]) {
+    float x[2 * kPairs<V>];
+#pragma unroll
+    for (int i = 0; i < kPairs<V>; ++i) up2(v[i], x[2 * i], x[2 * i + 1]);
+    unsigned a, b;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(sm100::smem_u32(p)), "r"(rank));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(sm100::smem_u32(bar)), "r"(rank));
     if constexpr (V == 4)
-        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3])
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(a),
+                     "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "r"(b)
                      : "memory");
     else if constexpr (V == 2)
-        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(x[0]), "f"(x[1]) : "memory");
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(a), "f"(x[0]),
+                     "f"(x[1]), "r"(b)
+                     : "memory");
     else
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(x[0]) : "memory");
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(a), "f"(x[0]), "r"(b)
+                     : "memory");
+}
+// waits, for at most limit_ns, until the phase of `bar` with this parity has completed: the bytes of every block of the
+// cluster are there to be read.  A limit shorter than the global timer's steps is over at the first test that fails.
+__device__ __forceinline__ bool wait_remote(uint64_t *bar, unsigned parity, uint64_t limit_ns) {
+    constexpr uint64_t kTimerStep = 1024;
+    unsigned ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(sm100::smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (limit_ns < kTimerStep) return false;
+    const uint64_t t0 = sm100::global_ns();
+    for (;;) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.b32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(sm100::smem_u32(bar)), "r"(parity), "r"(limit_ns < 0x10000ull ? (unsigned)limit_ns : 0x10000u)
+            : "memory");
+        if (ok) return true;
+        if (sm100::global_ns() - t0 >= limit_ns) return false;
+    }
 }
 
 // ---- the cut -------------------------------------------------------------------------------------------------------
@@ -109,29 +226,28 @@ struct Cut {
     int lx;     // lanes side by side over the channels, a power of two
     int slabs;  // tiles over the channels
     int ranks;  // blocks of a cluster: consecutive tiles in time
-    __host__ __device__ int tile() const { return kSteps * (kThreads / lx); }  // tokens of a tile
 };
 
 // Lanes over the channels: as many as leave the fewest of them idle on this D.  Fewer where that leaves the GPU without
-// two blocks for every SM, and blocks in clusters where that still does (a tile that no token reaches is never made).
-inline Cut choose_cut(long long rows, int D, int V, int S, int max_lx, int sms) {
+// two blocks for every SM, then blocks in clusters where that still does (a tile that no token reaches is never made).
+// Lanes down to min_lx come last: a row of so few channels is a sector or two of DRAM.
+inline Cut choose_cut(long long rows, int D, int V, int S, int TS, int max_lx, int min_lx, int sms) {
     Cut c{};
+    auto slabs_of = [&](int lx) { return (D + (long long)lx * V - 1) / ((long long)lx * V); };
     long long best = -1;
-    for (int lx = max_lx; lx >= 4; lx /= 2) {
-        const long long slabs = (D + (long long)lx * V - 1) / ((long long)lx * V);
-        if (best < 0 || slabs * lx < best) {
-            best = slabs * lx;
+    for (int lx = max_lx; lx >= min_lx; lx /= 2)
+        if (best < 0 || slabs_of(lx) * lx < best) {
+            best = slabs_of(lx) * lx;
             c.lx = lx;
-            c.slabs = (int)slabs;
         }
-    }
     const long long want = 2LL * sms;
-    while (c.lx > 8 && rows * c.slabs * 2 <= want && c.tile() < S) {
-        c.lx /= 2;
-        c.slabs = (int)((D + (long long)c.lx * V - 1) / ((long long)c.lx * V));
-    }
+    auto tile = [&] { return (long long)TS * (kThreads / c.lx); };
+    auto room = [&] { return rows * slabs_of(c.lx) * c.ranks * 2 <= want && c.ranks * tile() < S; };
     c.ranks = 1;
-    while (c.ranks < kMaxRanks && rows * c.slabs * c.ranks * 2 <= want && (long long)c.ranks * c.tile() < S) c.ranks *= 2;
+    while (c.lx > 8 && room()) c.lx /= 2;
+    while (c.ranks < kMaxRanks && room()) c.ranks *= 2;
+    while (c.lx > min_lx && room()) c.lx /= 2;
+    c.slabs = (int)slabs_of(c.lx);
     return c;
 }
 

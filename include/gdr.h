@@ -376,8 +376,8 @@ size_t gdr_conv1d_bwd_workspace(int B, int S, int Nk, int Nv, int Dk, int Dv, in
  *   final_state          device fp32 (B, N, D) or NULL: the state after token L_b - 1.  May alias initial_state
  *   checkpoints          device fp32 (B, N, ceil(S / 64), D) or NULL: the state before token 64 c of each chunk c, for
  *                        gdr_scan_bwd.  Chunks with 64 c >= L_b (c > 0) are left as they were
- * Apart from final_state, no output may overlap an input.  Constraints: B, S >= 0; N, D >= 1; B * N * D < 2^31; any D
- * (sizes that are a multiple of 4 are faster); pointers 16-byte aligned.  A length outside [0, S] skips the sequence
+ * Apart from final_state, no output may overlap an input.  Constraints: B, S >= 0; N >= 1; 1 <= D <= 2^26; B * N * D <
+ * 2^31; any D (sizes that are a multiple of 4 are faster); pointers 16-byte aligned.  A length outside [0, S] skips the sequence
  * (out rows zero, final_state and checkpoints as they were) and sets GDR_DEVERR_LENGTH.
  */
 #define GDR_SCAN_ADD 0

@@ -196,6 +196,26 @@ def test_side_stream_and_graph():
     assert gdr.get_error() == 0
 
 
+def test_wait_for_another_block_that_runs_out():
+    """With the wait limit at 1 ns the blocks of a cluster give up waiting for one another: the calls end with
+    GDR_DEVERR_TIMEOUT, and the next ones are right."""
+    x, g, s0, r = draws(1, 1, 6000, 64, "f32", "f32", 570)
+    tx, tg, st = dev(x, "f32"), dev(g, "f32"), dev(s0, "f32")
+    want = gdr.scan_fwd(tx, tg, st, output_checkpoints=True)
+    wg = gdr.scan_bwd(tx, tg, want[2], tx, st)
+    gdr.set_wait_limit_ns(1)
+    try:
+        gdr.scan_fwd(tx, tg, st)
+        assert gdr.get_error() == gdr.DEVERR_TIMEOUT
+        gdr.scan_bwd(tx, tg, want[2], tx, st)
+        assert gdr.get_error() == gdr.DEVERR_TIMEOUT
+    finally:
+        gdr.set_wait_limit_ns(0)
+    for u, v in zip(gdr.scan_fwd(tx, tg, st) + gdr.scan_bwd(tx, tg, want[2], tx, st), want[:2] + (None,) + wg):
+        assert v is None or torch.equal(u, v)
+    assert gdr.get_error() == 0
+
+
 def test_prepared_calls():
     x, g, s0, _ = draws(2, 2, 100, 64, "bf16", "f32", 560)
     tx, tg, st = dev(x, "bf16"), dev(g, "f32"), dev(s0, "f32")
