@@ -38,7 +38,7 @@ unsigned int g_snap_next = 0;          // next snapshot slot (under g_mu)
 int g_sm_count[kMaxDevices];           // multiprocessors per device (0 until first asked)
 int g_chunk_schedule = 0;              // tensor-core prefill schedule: 0 by shape, 1 one kernel, 2 two kernels
 
-bool supported_head(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
+}  // namespace
 
 // Multiprocessors of the current device; 148 (a full B200) when no device can be asked, so that the workspace
 // query answers the same on a machine without a GPU.
@@ -59,6 +59,10 @@ int sm_count() {
     }
     return g_sm_count[dev];
 }
+
+namespace {
+
+bool supported_head(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 
 // The tensor-core prefill's two-kernel schedule (a WY pass over every chunk on every SM, then the chains) pays
 // off when the (b, value head) chains occupy at most a third of the SMs: the one-kernel schedule would leave the

@@ -79,6 +79,9 @@ class LaunchCache {
     int grid_[kMaxDevices] = {};
 };
 
+// multiprocessors of the current device; 148 (a full B200) when no device can be asked
+int sm_count();
+
 cudaError_t launch_decode(const DecodeArgs &a, int Dk, int Dv, gdr_dtype dt, gdr_dtype st, cudaStream_t s);
 // The tensor-core prefill (bf16 / fp16, Dk = Dv = 128) has two schedules:
 //   chunk_tc.cu  one kernel, one CTA per (b, value head) chain that also solves each chunk's WY system; needs no

@@ -10,26 +10,31 @@ namespace gdr {
 namespace {
 using namespace scan;
 
-constexpr int kSteps = 4;   // tokens of a thread in a tile: decays, states and gradients of a segment stay in registers
-constexpr int kMaxLx = 16;  // so that a tile holds whole chunks
+// kWide: all 32 lanes of a warp lie over the channels, a segment is a warp and no shuffles are needed.  A tile has to hold
+// whole chunks, which it does then with 8 tokens a thread.
+// tokens of a thread in a tile, and blocks of an SM: decays, states and gradients of a segment stay in registers
+template <typename T, bool kMix> constexpr int kStepsOf = sizeof(T) == 2 && !kMix ? 8 : 4;
+template <typename T, bool kMix> constexpr int kBlocksOf = sizeof(T) == 2 && !kMix ? 2 : kMix ? 2 : 3;
 
-template <typename T, typename G, int V> struct Layout {
-    static constexpr int kCh = kMaxLx * V;
+template <typename T, typename G, int V, int kSteps, bool kWide> struct Layout {
+    static constexpr int kCh = (kWide ? 32 : 16) * V;
     RawV<G, V> g[kSteps][kThreads];
     RawV<T, V> x[kSteps][kThreads], d[kSteps][kThreads];
+    RawV<float, V> h[kThreads];  // the state before the segment's chunk
     float wa[2][kWarps][kCh], wf[2][kWarps][kCh], wr[2][kWarps][kCh];  // A and the forward and backward B of every warp
     float ca[2][kMaxRanks][kCh], cr[2][kMaxRanks][kCh];                // A and the backward B of every block of the cluster
     uint64_t arrived[2];
 };
 
-template <typename T, typename G, bool kMix, int V>
-__global__ void __launch_bounds__(kThreads, kMix ? 2 : 3) scan_bwd_kernel(const ScanBwdArgs a, const Cut cut) {
+template <typename T, typename G, bool kMix, int V, bool kWide>
+__global__ void __launch_bounds__(kThreads, (kBlocksOf<T, kMix>)) scan_bwd_kernel(const ScanBwdArgs a, const Cut cut) {
     extern __shared__ __align__(16) unsigned char smem[];
-    auto &sm = *reinterpret_cast<Layout<T, G, V> *>(smem);
+    constexpr int kSteps = kStepsOf<T, kMix>;
+    auto &sm = *reinterpret_cast<Layout<T, G, V, kSteps, kWide> *>(smem);
     constexpr int P = kPairs<V>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int lx = cut.lx, cl = lane & (lx - 1);
-    const int seg = tid / lx;
+    const int lx = kWide ? 32 : cut.lx, cl = lane & (lx - 1);
+    const int seg = kWide ? warp : tid / lx;
     const int R = cut.ranks, rank = (int)(blockIdx.x % R);
     const long long unit = blockIdx.x / R;
     const int slab = (int)(unit % cut.slabs);
@@ -56,7 +61,8 @@ __global__ void __launch_bounds__(kThreads, kMix ? 2 : 3) scan_bwd_kernel(const 
     const int TT = kSteps * (kThreads / lx);
     const long long step = (long long)R * TT;
     const int tiles = (int)((L + step - 1) / step);
-    const int chunk_warps = lx > 2 ? lx / 2 : 1;  // warps of a chunk: 64 / kSteps segments, 32 / lx of them a warp
+    constexpr int kSegs = kChunk / kSteps;  // segments of a chunk
+    const int chunk_warps = kSegs * lx > 32 ? kSegs * lx / 32 : 1;  // warps of a chunk: no warp holds more than one
     const unsigned exchange = (unsigned)(R * lx * V * 2 * sizeof(float));
     bool lost = false;
     if (R > 1) {
@@ -68,33 +74,54 @@ __global__ void __launch_bounds__(kThreads, kMix ? 2 : 3) scan_bwd_kernel(const 
         cluster_meet();
     }
 
+    // rows of whole 16 bytes are staged by the warp (stage_rows)
+    const bool by_warp = kWide && (a.D & 7) == 0;
+    const long long left = ((long long)a.D - slab * 32 * V) * 2;  // bytes of a row of 16-bit elements from the slab on
     auto fetch = [&](int k) {
         const long long t0 = k * step + (long long)rank * TT + seg * kSteps;
-        const int n = on ? (int)max(0LL, min((long long)kSteps, L - t0)) : 0;
-        const size_t at = n > 0 ? (size_t)t0 : 0;
-        stage_segment<kSteps>(sm.g, g + at * row_g, row_g, n);
-        stage_segment<kSteps>(sm.x, x + at * row_x, row_x, n);
-        stage_segment<kSteps>(sm.d, d + at * row_x, row_x, n);
+        const int nt = (int)max(0LL, min((long long)kSteps, L - t0)), n = on ? nt : 0;
+        const size_t at = nt > 0 ? (size_t)t0 : 0;
+        if constexpr (kWide && sizeof(G) * V == 8) {
+            if (by_warp) stage_rows<kSteps>(sm.g, g + at * row_g - lane * 8, row_g, nt, left);
+            else stage_segment<kSteps>(sm.g, g + at * row_g, row_g, n);
+        } else {
+            stage_segment<kSteps>(sm.g, g + at * row_g, row_g, n);
+        }
+        if constexpr (kWide && sizeof(T) * V == 8) {
+            if (by_warp) stage_rows<kSteps>(sm.x, x + at * row_x - lane * 8, row_x, nt, left);
+            else stage_segment<kSteps>(sm.x, x + at * row_x, row_x, n);
+        } else {
+            stage_segment<kSteps>(sm.x, x + at * row_x, row_x, n);
+        }
+        if constexpr (kWide && sizeof(T) * V == 8) {
+            if (by_warp) stage_rows<kSteps>(sm.d, d + at * row_x - lane * 8, row_x, nt, left);
+            else stage_segment<kSteps>(sm.d, d + at * row_x, row_x, n);
+        } else {
+            stage_segment<kSteps>(sm.d, d + at * row_x, row_x, n);
+        }
+        const long long chunk = t0 / kChunk;
+        const bool has = on && chunk * kChunk < L;
+        stage<RawV<float, V>, true>(&sm.h[tid], ck + (has ? (size_t)chunk * a.D : 0), has);
         stage_commit();
     };
     if (tiles > 0) fetch(tiles - 1);
     for (int k = tiles - 1, n = 0; k >= 0; --k, ++n) {
         const int p = n & 1;
         const long long t0 = k * step + (long long)rank * TT + seg * kSteps;
-        f2_t h[P];  // the state before the chunk
-        fill(h, 0.f);
-        const long long chunk = t0 / kChunk;
-        if (on && chunk * kChunk < L) load_f32<V>(ck + (size_t)chunk * a.D, h);
         // a segment forwards, (A, F): h -> A h + F, and backwards, (A, B): mu -> A mu + B; behind the sequence a = 1 and
         // x = dout = 0, which changes neither
-        f2_t av[kSteps][P], rest[kMix ? kSteps : 1][P], xv[kSteps][P], dv[kSteps][P], A[P], F[P], B[P];
+        f2_t av[kSteps][P], rest[kMix ? kSteps : 1][P], xv[kSteps][P], A[P], F[P], B[P];
+        RawV<T, V> dr[kSteps];
         stage_wait();
+        if (kWide) __syncwarp();
+        f2_t h[P];
+        unpack<float, V>(sm.h[tid], h);
 #pragma unroll
         for (int j = 0; j < kSteps; ++j) {
             f2_t gv[P];
             unpack<G, V>(sm.g[j][tid], gv);
             unpack<T, V>(sm.x[j][tid], xv[j]);
-            unpack<T, V>(sm.d[j][tid], dv[j]);
+            dr[j] = sm.d[j][tid];
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 f2_t r;
@@ -106,46 +133,53 @@ __global__ void __launch_bounds__(kThreads, kMix ? 2 : 3) scan_bwd_kernel(const 
             }
         }
 #pragma unroll
-        for (int j = kSteps - 1; j >= 0; --j)
+        for (int j = kSteps - 1; j >= 0; --j) {
+            f2_t dv[P];
+            unpack<T, V>(dr[j], dv);
 #pragma unroll
-            for (int i = 0; i < P; ++i) B[i] = mul2(av[j][i], j < kSteps - 1 ? add2(dv[j][i], B[i]) : dv[j][i]);
-        // over the segments of the warp: (EA, EF) those before this one, (LA, LB) those behind it
-        f2_t EA[P], EF[P], LA[P], LB[P], TA[P], TF[P], TB[P];
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            TA[i] = LA[i] = A[i];
-            TF[i] = F[i];
-            TB[i] = B[i];
+            for (int i = 0; i < P; ++i) B[i] = mul2(av[j][i], j < kSteps - 1 ? add2(dv[i], B[i]) : dv[i]);
         }
-        for (int q = lx; q < 32; q *= 2) {
+        if (kWide) __syncwarp();
+        if (k > 0) fetch(k - 1);  // what this thread (this warp) copied for itself is in registers
+        // over the segments of the warp: (EA, EF) those before this one, (LA, LB) those behind it
+        f2_t EA[P], EF[P], LA[P], LB[P];
+        if constexpr (!kWide) {
+            f2_t TA[P];
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const f2_t pa = shfl_up2(TA[i], q), pf = shfl_up2(TF[i], q);
-                if (lane >= q) {
-                    TF[i] = fma2(TA[i], pf, TF[i]);
-                    TA[i] = mul2(TA[i], pa);
-                }
-                const f2_t na = shfl_down2(LA[i], q), nb = shfl_down2(TB[i], q);
-                if (lane + q < 32) {
-                    TB[i] = fma2(LA[i], nb, TB[i]);
-                    LA[i] = mul2(LA[i], na);
+            for (int i = 0; i < P; ++i) TA[i] = LA[i] = A[i];
+            for (int q = lx; q < 32; q *= 2) {
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const f2_t pa = shfl_up2(TA[i], q), pf = shfl_up2(F[i], q);
+                    if (lane >= q) {
+                        F[i] = fma2(TA[i], pf, F[i]);
+                        TA[i] = mul2(TA[i], pa);
+                    }
+                    const f2_t na = shfl_down2(LA[i], q), nb = shfl_down2(B[i], q);
+                    if (lane + q < 32) {
+                        B[i] = fma2(LA[i], nb, B[i]);
+                        LA[i] = mul2(LA[i], na);
+                    }
                 }
             }
-        }
-        if (lane >= 32 - lx) {
-            store<float, V>(&sm.wa[p][warp][cl * V], TA);
-            store<float, V>(&sm.wf[p][warp][cl * V], TF);
-        }
-        if (lane < lx) store<float, V>(&sm.wr[p][warp][cl * V], TB);
+            if (lane >= 32 - lx) {
+                store<float, V>(&sm.wa[p][warp][cl * V], TA);
+                store<float, V>(&sm.wf[p][warp][cl * V], F);
+            }
+            if (lane < lx) store<float, V>(&sm.wr[p][warp][cl * V], B);
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            EA[i] = shfl_up2(TA[i], lx);
-            EF[i] = shfl_up2(TF[i], lx);
-            LA[i] = shfl_down2(LA[i], lx);
-            LB[i] = shfl_down2(TB[i], lx);
+            for (int i = 0; i < P; ++i) {
+                EA[i] = shfl_up2(TA[i], lx);
+                EF[i] = shfl_up2(F[i], lx);
+                LA[i] = shfl_down2(LA[i], lx);
+                LB[i] = shfl_down2(B[i], lx);
+            }
+        } else {
+            store<float, V>(&sm.wa[p][warp][cl * V], A);
+            store<float, V>(&sm.wf[p][warp][cl * V], F);
+            store<float, V>(&sm.wr[p][warp][cl * V], B);
         }
         __syncthreads();
-        if (k > 0) fetch(k - 1);
         if (R > 1) {  // as in the forward kernel, the block's backward map to every block of the cluster
             if (tid == 0) sm100::mbar_arrive_expect_tx(&sm.arrived[p], exchange);
             if (warp < R && lane < lx) {
@@ -176,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, kMix ? 2 : 3) scan_bwd_kernel(const 
 #pragma unroll
             for (int i = 0; i < P; ++i) h[i] = fma2(wa[i], h[i], wf[i]);
         }
-        if (lane >= lx) {
+        if (!kWide && lane >= lx) {
 #pragma unroll
             for (int i = 0; i < P; ++i) h[i] = fma2(EA[i], h[i], EF[i]);
         }
@@ -195,53 +229,78 @@ __global__ void __launch_bounds__(kThreads, kMix ? 2 : 3) scan_bwd_kernel(const 
         }
         // what comes back to this segment: from behind the tiles, the later blocks, the later warps, the later segments
         f2_t m[P];
+        if (R > 1) {
+            for (int r = R - 1; r >= 0; --r) {
+                if (r == rank) {
 #pragma unroll
-        for (int i = 0; i < P; ++i) m[i] = mu[i];
-        for (int r = R - 1; r >= 0 && R > 1; --r) {
-            f2_t ra[P], rb[P];
-            load_f32<V>(&sm.ca[p][r][cl * V], ra);
-            load_f32<V>(&sm.cr[p][r][cl * V], rb);
+                    for (int i = 0; i < P; ++i) m[i] = mu[i];
+                }
+                f2_t ra[P], rb[P];
+                load_f32<V>(&sm.ca[p][r][cl * V], ra);
+                load_f32<V>(&sm.cr[p][r][cl * V], rb);
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                mu[i] = fma2(ra[i], mu[i], rb[i]);
-                if (r > rank) m[i] = mu[i];
+                for (int i = 0; i < P; ++i) mu[i] = fma2(ra[i], mu[i], rb[i]);
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < P; ++i) m[i] = mu[i];
         }
 #pragma unroll
-        for (int w = kWarps - 1; w >= 0; --w) {
-            if (R > 1 && w <= warp) break;
+        for (int w = kWarps - 1; w > 0; --w) {
+            if (w <= warp) break;
             f2_t wa[P], wb[P];
             load_f32<V>(&sm.wa[p][w][cl * V], wa);
             load_f32<V>(&sm.wr[p][w][cl * V], wb);
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                if (R > 1) {
-                    m[i] = fma2(wa[i], m[i], wb[i]);
-                } else {
-                    mu[i] = fma2(wa[i], mu[i], wb[i]);
-                    if (w > warp) m[i] = mu[i];
-                }
+            for (int i = 0; i < P; ++i) m[i] = fma2(wa[i], m[i], wb[i]);
+        }
+        if (R == 1) {  // the whole tile: on through this warp and the earlier ones
+#pragma unroll
+            for (int i = 0; i < P; ++i) mu[i] = m[i];
+#pragma unroll
+            for (int w = kWarps - 1; w >= 0; --w) {
+                if (w > warp) continue;
+                f2_t wa[P], wb[P];
+                load_f32<V>(&sm.wa[p][w][cl * V], wa);
+                load_f32<V>(&sm.wr[p][w][cl * V], wb);
+#pragma unroll
+                for (int i = 0; i < P; ++i) mu[i] = fma2(wa[i], mu[i], wb[i]);
             }
         }
-        if (lane + lx < 32) {
+        if (!kWide && lane + lx < 32) {
 #pragma unroll
             for (int i = 0; i < P; ++i) m[i] = fma2(LA[i], m[i], LB[i]);
         }
-        if (on && t0 < a.S) {
-            const int ns = (int)min((long long)kSteps, a.S - t0), nv = (int)max(0LL, min((long long)kSteps, L - t0));
-            char *ox = dx + (size_t)t0 * row_x, *og = dg + (size_t)t0 * row_g;
+        char *ox = dx + (size_t)t0 * row_x, *og = dg + (size_t)t0 * row_g;
+        auto back = [&](int j, f2_t (&rx)[P], f2_t (&rg)[P]) {
+            f2_t dv[P];
+            unpack<T, V>(dr[j], dv);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const f2_t lam = add2(dv[i], m[i]);
+                m[i] = mul2(av[j][i], lam);
+                rx[i] = kMix ? mul2(rest[kMix ? j : 0][i], lam) : lam;
+                rg[i] = mul2(m[i], xv[j][i]);
+            }
+        };
+        if (on && t0 + kSteps <= L) {
 #pragma unroll
             for (int j = kSteps - 1; j >= 0; --j) {
                 f2_t rx[P], rg[P];
+                back(j, rx, rg);
+                store<T, V>(ox + j * (size_t)row_x, rx);
+                store<G, V>(og + j * (size_t)row_g, rg);
+            }
+        } else if (on) {
 #pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    const f2_t lam = add2(dv[j][i], m[i]);
-                    m[i] = mul2(av[j][i], lam);
-                    rx[i] = kMix ? mul2(rest[kMix ? j : 0][i], lam) : lam;
-                    rg[i] = mul2(m[i], xv[j][i]);
-                    if (j >= nv) rx[i] = rg[i] = 0;
+            for (int j = kSteps - 1; j >= 0; --j) {
+                f2_t rx[P], rg[P];
+                back(j, rx, rg);
+                if (t0 + j >= L) {
+                    fill(rx, 0.f);
+                    fill(rg, 0.f);
                 }
-                if (j < ns) {
+                if (t0 + j < a.S) {
                     store<T, V>(ox + j * (size_t)row_x, rx);
                     store<G, V>(og + j * (size_t)row_g, rg);
                 }
@@ -259,32 +318,29 @@ __global__ void __launch_bounds__(kThreads, kMix ? 2 : 3) scan_bwd_kernel(const 
     if (a.dinitial_state && seg == 0 && rank == 0) store<float, V>(a.dinitial_state + (size_t)bn * a.D + c0, mu);
 }
 
-template <typename T, typename G, bool kMix, int V> cudaError_t launch_v(const ScanBwdArgs &a, cudaStream_t s) {
-    static LaunchCache cache(reinterpret_cast<const void *>(scan_bwd_kernel<T, G, kMix, V>));
-    const int smem = (int)sizeof(Layout<T, G, V>);
-    int grid = 0;
-    cudaError_t e = cache.allow_smem(smem);
-    if (e == cudaSuccess) e = cache.resident_grid(kThreads, smem, &grid);
+template <typename T, typename G, bool kMix, int V, bool kWide>
+cudaError_t launch_v(const ScanBwdArgs &a, const Cut &cut, cudaStream_t s) {
+    static LaunchCache cache(reinterpret_cast<const void *>(scan_bwd_kernel<T, G, kMix, V, kWide>));
+    const int smem = (int)sizeof(Layout<T, G, V, kStepsOf<T, kMix>, kWide>);
+    const cudaError_t e = cache.allow_smem(smem);
     if (e != cudaSuccess) return e;
-    const Cut cut = choose_cut((long long)a.B * a.N, a.D, V, a.S, kSteps, kMaxLx, 2, grid / (kMix ? 2 : 3));
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((long long)a.B * a.N * cut.slabs * cut.ranks));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = cut.ranks;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = cut.ranks > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, scan_bwd_kernel<T, G, kMix, V>, a, cut);
+    return launch_clusters(scan_bwd_kernel<T, G, kMix, V, kWide>, (long long)a.B * a.N, cut, smem, a, s);
 }
 
+// vectors of 4 channels where rows are made of whole ones, of 2, else single channels
 template <typename T, typename G, bool kMix> cudaError_t launch_m(const ScanBwdArgs &a, cudaStream_t s) {
-    if (a.D % 4 == 0) return launch_v<T, G, kMix, 4>(a, s);
-    if (a.D % 2 == 0) return launch_v<T, G, kMix, 2>(a, s);
-    return launch_v<T, G, kMix, 1>(a, s);
+    constexpr int kSteps = kStepsOf<T, kMix>, kMin = 32 * kSteps / kChunk;
+    constexpr bool kCanBeWide = kSteps == 8;
+    const long long rows = (long long)a.B * a.N;
+    const int blocks = kBlocksOf<T, kMix> * sm_count();
+    if (a.D % 4 == 0) {
+        const Cut cut = choose_cut(rows, a.D, 4, a.S, kSteps, kCanBeWide ? 32 : 16, kMin, blocks);
+        if constexpr (kCanBeWide)
+            if (cut.lx == 32) return launch_v<T, G, kMix, 4, true>(a, cut, s);
+        return launch_v<T, G, kMix, 4, false>(a, cut, s);
+    }
+    if (a.D % 2 == 0) return launch_v<T, G, kMix, 2, false>(a, choose_cut(rows, a.D, 2, a.S, kSteps, 16, kMin, blocks), s);
+    return launch_v<T, G, kMix, 1, false>(a, choose_cut(rows, a.D, 1, a.S, kSteps, 16, kMin, blocks), s);
 }
 template <typename T, typename G> cudaError_t launch_t(const ScanBwdArgs &a, cudaStream_t s) {
     return a.mode == GDR_SCAN_MIX ? launch_m<T, G, true>(a, s) : launch_m<T, G, false>(a, s);

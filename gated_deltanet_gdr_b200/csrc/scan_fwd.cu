@@ -11,8 +11,9 @@ using namespace scan;
 
 constexpr int kSteps = 8;  // tokens of a thread in a tile
 
-template <typename T, typename G, int V> struct Layout {
-    static constexpr int kCh = 32 * V;  // most channels of a tile
+// kWide: all 32 lanes of a warp lie over the channels, a segment is a warp and no shuffles are needed
+template <typename T, typename G, int V, bool kWide> struct Layout {
+    static constexpr int kCh = (kWide ? 32 : 16) * V;  // most channels of a tile
     RawV<G, V> g[kSteps][kThreads];
     RawV<T, V> x[kSteps][kThreads];
     float wa[2][kWarps][kCh], wb[2][kWarps][kCh];        // (A, B) of every warp, for even and odd tiles
@@ -20,13 +21,13 @@ template <typename T, typename G, int V> struct Layout {
     uint64_t arrived[2];                                 // their bytes
 };
 
-template <typename T, typename G, bool kMix, int V>
+template <typename T, typename G, bool kMix, int V, bool kWide>
 __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a, const Cut cut) {
     extern __shared__ __align__(16) unsigned char smem[];
-    auto &sm = *reinterpret_cast<Layout<T, G, V> *>(smem);
+    auto &sm = *reinterpret_cast<Layout<T, G, V, kWide> *>(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int lx = cut.lx, cl = lane & (lx - 1);
-    const int seg = tid / lx;  // lanes of a segment are adjacent
+    const int lx = kWide ? 32 : cut.lx, cl = lane & (lx - 1);
+    const int seg = kWide ? warp : tid / lx;  // lanes of a segment are adjacent
     const int R = cut.ranks, rank = (int)(blockIdx.x % R);
     const long long unit = blockIdx.x / R;
     const int slab = (int)(unit % cut.slabs);
@@ -65,12 +66,25 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
         cluster_meet();  // every block of the cluster has started, with its barriers ready
     }
 
+    // rows of whole 16 bytes are staged by the warp (stage_rows)
+    const bool by_warp = kWide && (a.D & 7) == 0;
+    const long long left = ((long long)a.D - slab * 32 * V) * 2;  // bytes of a row of 16-bit elements from the slab on
     auto fetch = [&](int k) {
         const long long t0 = k * step + (long long)rank * TT + seg * kSteps;
-        const int n = on ? (int)max(0LL, min((long long)kSteps, L - t0)) : 0;
-        const size_t at = n > 0 ? (size_t)t0 : 0;
-        stage_segment<kSteps>(sm.g, g + at * row_g, row_g, n);
-        stage_segment<kSteps>(sm.x, x + at * row_x, row_x, n);
+        const int nt = (int)max(0LL, min((long long)kSteps, L - t0)), n = on ? nt : 0;
+        const size_t at = nt > 0 ? (size_t)t0 : 0;
+        if constexpr (kWide && sizeof(G) * V == 8) {
+            if (by_warp) stage_rows<kSteps>(sm.g, g + at * row_g - lane * 8, row_g, nt, left);
+            else stage_segment<kSteps>(sm.g, g + at * row_g, row_g, n);
+        } else {
+            stage_segment<kSteps>(sm.g, g + at * row_g, row_g, n);
+        }
+        if constexpr (kWide && sizeof(T) * V == 8) {
+            if (by_warp) stage_rows<kSteps>(sm.x, x + at * row_x - lane * 8, row_x, nt, left);
+            else stage_segment<kSteps>(sm.x, x + at * row_x, row_x, n);
+        } else {
+            stage_segment<kSteps>(sm.x, x + at * row_x, row_x, n);
+        }
         stage_commit();
     };
     if (tiles > 0) fetch(0);
@@ -80,6 +94,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
         // decays and writes of the segment (tokens behind the sequence: a = 1, b = 0), and the segment as a whole
         f2_t av[kSteps][P], bv[kSteps][P], A[P], B[P];
         stage_wait();
+        if (kWide) __syncwarp();
 #pragma unroll
         for (int j = 0; j < kSteps; ++j) {
             f2_t gv[P];
@@ -94,11 +109,13 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
                 B[i] = j ? fma2(av[j][i], B[i], bv[j][i]) : bv[j][i];
             }
         }
+        if (kWide) __syncwarp();
+        if (k + 1 < tiles) fetch(k + 1);  // what this thread (this warp) copied for itself is in registers
         // inclusive composition over the segments of the warp; (EA, EB): the segments before this one
         f2_t EA[P], EB[P];
         fill(EA, 1.f);
         fill(EB, 0.f);
-        if (lx < 32) {
+        if (!kWide) {
             for (int d = lx; d < 32; d *= 2) {
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
@@ -123,7 +140,6 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
             store<float, V>(&sm.wb[p][warp][cl * V], B);
         }
         __syncthreads();
-        if (k + 1 < tiles) fetch(k + 1);  // every thread has taken its own inputs out of the stage
         if (R > 1) {
             // the block as a whole to every block of the cluster, one warp for each.  A block writes a place again two
             // tiles on, having received the tile between, which its owner sent after reading this one.
@@ -182,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
                 }
             }
         }
-        if (lx < 32) {
+        if (!kWide) {
 #pragma unroll
             for (int i = 0; i < P; ++i) hs[i] = fma2(EA[i], hs[i], EB[i]);
         }
@@ -218,33 +234,25 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
     if (a.final_state && Lr >= 0 && seg == 0 && rank == 0) store<float, V>(a.final_state + (size_t)bn * a.D + c0, h);
 }
 
-template <typename T, typename G, bool kMix, int V> cudaError_t launch_v(const ScanArgs &a, cudaStream_t s) {
-    static LaunchCache cache(reinterpret_cast<const void *>(scan_fwd_kernel<T, G, kMix, V>));
-    const int smem = (int)sizeof(Layout<T, G, V>);
-    int grid = 0;
-    cudaError_t e = cache.allow_smem(smem);
-    if (e == cudaSuccess) e = cache.resident_grid(kThreads, smem, &grid);  // two blocks an SM
+template <typename T, typename G, bool kMix, int V, bool kWide>
+cudaError_t launch_v(const ScanArgs &a, const Cut &cut, cudaStream_t s) {
+    static LaunchCache cache(reinterpret_cast<const void *>(scan_fwd_kernel<T, G, kMix, V, kWide>));
+    const int smem = (int)sizeof(Layout<T, G, V, kWide>);
+    const cudaError_t e = cache.allow_smem(smem);
     if (e != cudaSuccess) return e;
-    const Cut cut = choose_cut((long long)a.B * a.N, a.D, V, a.S, kSteps, 32, 4, grid / 2);
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((long long)a.B * a.N * cut.slabs * cut.ranks));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = cut.ranks;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = cut.ranks > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, scan_fwd_kernel<T, G, kMix, V>, a, cut);
+    return launch_clusters(scan_fwd_kernel<T, G, kMix, V, kWide>, (long long)a.B * a.N, cut, smem, a, s);
 }
 
 // vectors of 4 channels where rows are made of whole ones, of 2, else single channels
 template <typename T, typename G, bool kMix> cudaError_t launch_m(const ScanArgs &a, cudaStream_t s) {
-    if (a.D % 4 == 0) return launch_v<T, G, kMix, 4>(a, s);
-    if (a.D % 2 == 0) return launch_v<T, G, kMix, 2>(a, s);
-    return launch_v<T, G, kMix, 1>(a, s);
+    const long long rows = (long long)a.B * a.N;
+    const int blocks = 2 * sm_count();
+    if (a.D % 4 == 0) {
+        const Cut cut = choose_cut(rows, a.D, 4, a.S, kSteps, 32, 4, blocks);
+        return cut.lx == 32 ? launch_v<T, G, kMix, 4, true>(a, cut, s) : launch_v<T, G, kMix, 4, false>(a, cut, s);
+    }
+    if (a.D % 2 == 0) return launch_v<T, G, kMix, 2, false>(a, choose_cut(rows, a.D, 2, a.S, kSteps, 16, 4, blocks), s);
+    return launch_v<T, G, kMix, 1, false>(a, choose_cut(rows, a.D, 1, a.S, kSteps, 16, 4, blocks), s);
 }
 template <typename T, typename G> cudaError_t launch_t(const ScanArgs &a, cudaStream_t s) {
     return a.mode == GDR_SCAN_MIX ? launch_m<T, G, true>(a, s) : launch_m<T, G, false>(a, s);

@@ -42,38 +42,34 @@ __device__ __forceinline__ float ex2(float x) {
 // of a rounding (2^-24) of a for |g| < 1/8, or below one rounding of the rest for |g| < 1/4: the rest keeps its digits, and
 // a decay close to 1 is good to a rounding -- it is applied hundreds of times, and what ex2.approx loses (up to 2^-22)
 // would add up.  Elsewhere ex2(g log2 e), whose argument is rounded once more (|g| 2^-24): there a state fades soon.
-template <bool kRest> __device__ __forceinline__ void decay(f2_t g, f2_t &a, f2_t &rest) {
-    f2_t near_a, near_rest = 0;
+template <bool kRest> __device__ __forceinline__ void decay(float g, float &a, float &rest) {
+    const float far = ex2(g * 1.4426950408889634f);
     if (kRest) {  // -g (1 + g/2 + ... + g^5/720)
-        f2_t p = both(-1.f / 720.f);
-        p = fma2(p, g, both(-1.f / 120.f));
-        p = fma2(p, g, both(-1.f / 24.f));
-        p = fma2(p, g, both(-1.f / 6.f));
-        p = fma2(p, g, both(-0.5f));
-        p = fma2(p, g, both(-1.f));
-        near_rest = mul2(p, g);
-        near_a = fma2(near_rest, both(-1.f), both(1.f));
+        float p = fmaf(g, -1.f / 720.f, -1.f / 120.f);
+        p = fmaf(p, g, -1.f / 24.f);
+        p = fmaf(p, g, -1.f / 6.f);
+        p = fmaf(p, g, -0.5f);
+        p = fmaf(p, g, -1.f);
+        const float near = p * g;
+        const bool s = fabsf(g) < 0.25f;
+        rest = s ? near : 1.f - far;
+        a = s ? 1.f - near : far;
     } else {  // 1 + g + ... + g^5/120
-        f2_t p = both(1.f / 120.f);
-        p = fma2(p, g, both(1.f / 24.f));
-        p = fma2(p, g, both(1.f / 6.f));
-        p = fma2(p, g, both(0.5f));
-        p = fma2(p, g, both(1.f));
-        near_a = fma2(p, g, both(1.f));
+        float p = fmaf(g, 1.f / 120.f, 1.f / 24.f);
+        p = fmaf(p, g, 1.f / 6.f);
+        p = fmaf(p, g, 0.5f);
+        p = fmaf(p, g, 1.f);
+        p = fmaf(p, g, 1.f);
+        a = fabsf(g) < 0.125f ? p : far;
     }
-    const f2_t t = mul2(g, both(1.4426950408889634f));
-    constexpr float kNear = kRest ? 0.25f : 0.125f;
-    float g0, g1, t0, t1, n0, n1, r0, r1;
+}
+template <bool kRest> __device__ __forceinline__ void decay(f2_t g, f2_t &a, f2_t &rest) {
+    float g0, g1, a0, a1, r0 = 0.f, r1 = 0.f;
     up2(g, g0, g1);
-    up2(t, t0, t1);
-    up2(near_a, n0, n1);
-    const bool s0 = fabsf(g0) < kNear, s1 = fabsf(g1) < kNear;
-    const float f0 = ex2(t0), f1 = ex2(t1);
-    a = pk2(s0 ? n0 : f0, s1 ? n1 : f1);
-    if (kRest) {
-        up2(near_rest, r0, r1);
-        rest = pk2(s0 ? r0 : 1.f - f0, s1 ? r1 : 1.f - f1);
-    }
+    decay<kRest>(g0, a0, r0);
+    decay<kRest>(g1, a1, r1);
+    a = pk2(a0, a1);
+    rest = pk2(r0, r1);
 }
 
 // length of sequence b, or -1 for one outside [0, S]
@@ -163,6 +159,21 @@ __device__ __forceinline__ void stage_segment(R (*dst)[kThreads], const void *sr
         for (int j = 0; j < TS; ++j) stage<R, true>(&dst[j][threadIdx.x], j < n ? p + j * (size_t)row : p, j < n);
     }
 }
+// the same for a warp whose lanes lie side by side over 32 * 8 bytes of a row: 16 bytes a lane, two rows an instruction.  p is
+// the row's start at the warp's first channel, `bytes` what the row still holds there (a multiple of 16, may be <= 0).
+// Lanes read what others copied: __syncwarp() after the wait and before the next copy.
+template <int TS> __device__ __forceinline__ void stage_rows(uint2 (*dst)[kThreads], const char *p, unsigned row, int n, long long bytes) {
+    const int lane = threadIdx.x & 31, sub = lane >> 4, at = (lane & 15) * 16;
+    const bool on = at < bytes;
+#pragma unroll
+    for (int j = 0; j < TS; j += 2) {
+        const bool in = on && j + sub < n;
+        const unsigned d = (unsigned)__cvta_generic_to_shared(&dst[j + sub][threadIdx.x & ~31]) + at;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d),
+                     "l"(in ? p + (j + sub) * (size_t)row + at : p), "r"(in ? 16 : 0)
+                     : "memory");
+    }
+}
 __device__ __forceinline__ void stage_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void stage_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
@@ -228,27 +239,45 @@ struct Cut {
     int ranks;  // blocks of a cluster: consecutive tiles in time
 };
 
-// Lanes over the channels: as many as leave the fewest of them idle on this D.  Fewer where that leaves the GPU without
-// two blocks for every SM, then blocks in clusters where that still does (a tile that no token reaches is never made).
-// Lanes down to min_lx come last: a row of so few channels is a sector or two of DRAM.
-inline Cut choose_cut(long long rows, int D, int V, int S, int TS, int max_lx, int min_lx, int sms) {
+// Lanes over the channels: the most that leave at most a quarter more lanes idle on this D than the best choice does.
+// Where the `want` blocks that the GPU holds are then not even half there, first clusters of up to 4 blocks, then fewer
+// lanes, then clusters of 8 (measured, forward, us: 128 rows of 128 channels and 4096 tokens 95 with 32 lanes and 2 blocks, 98
+// with 16 and 1; 4096 channels and 8192 tokens 67 with 16 lanes and 4 blocks, 70 with 32 and 8; 640 channels and 32769
+// tokens 78 with 8 lanes and 8 blocks, 89 with 16).  Less than 8 lanes come last: a row of so few channels is a sector or two.  No
+// cluster has a block that no token reaches.
+inline Cut choose_cut(long long rows, int D, int V, int S, int TS, int max_lx, int min_lx, long long want) {
     Cut c{};
     auto slabs_of = [&](int lx) { return (D + (long long)lx * V - 1) / ((long long)lx * V); };
-    long long best = -1;
+    long long least = -1;
     for (int lx = max_lx; lx >= min_lx; lx /= 2)
-        if (best < 0 || slabs_of(lx) * lx < best) {
-            best = slabs_of(lx) * lx;
-            c.lx = lx;
-        }
-    const long long want = 2LL * sms;
+        if (least < 0 || slabs_of(lx) * lx < least) least = slabs_of(lx) * lx;
+    c.lx = max_lx;
+    while (slabs_of(c.lx) * c.lx * 4 > least * 5) c.lx /= 2;
     auto tile = [&] { return (long long)TS * (kThreads / c.lx); };
     auto room = [&] { return rows * slabs_of(c.lx) * c.ranks * 2 <= want && c.ranks * tile() < S; };
     c.ranks = 1;
+    while (c.ranks < 4 && room()) c.ranks *= 2;
     while (c.lx > 8 && room()) c.lx /= 2;
     while (c.ranks < kMaxRanks && room()) c.ranks *= 2;
     while (c.lx > min_lx && room()) c.lx /= 2;
     c.slabs = (int)slabs_of(c.lx);
     return c;
+}
+
+template <typename Args>
+cudaError_t launch_clusters(void (*kernel)(Args, Cut), long long rows, const Cut &cut, int smem, const Args &a, cudaStream_t s) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(rows * cut.slabs * cut.ranks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = cut.ranks;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = cut.ranks > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, a, cut);
 }
 
 }  // namespace scan
