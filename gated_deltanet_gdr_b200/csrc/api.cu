@@ -411,6 +411,8 @@ extern "C" int gdr_conv1d_bwd(const void *x, const void *weight, const void *bia
     if (st) return st;
     if (K < 1 || K > 8) return GDR_ERR_SHAPE;
     if (B > 65535 || (long long)S > 65535LL * 64) return GDR_ERR_SHAPE;  // as gdr_conv1d
+    // a row's bytes are kept in 32 bits
+    if (2LL * Nk * Dk + 1LL * Nv * Dv > 1LL << 26) return GDR_ERR_SHAPE;
     if (!dweight) return GDR_ERR_NULL;
     if ((long long)B * S > 0 && (!x || !weight || !dq || !dk || !dv || !dx)) return GDR_ERR_NULL;
     if (B > 0 && dconv_state_in && !weight) return GDR_ERR_NULL;

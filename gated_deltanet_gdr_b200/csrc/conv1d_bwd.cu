@@ -4,49 +4,25 @@
 // dx[t] = sum_j w_j dpre[t + K - 1 - j];  dw_j = sum_u dpre[u] x[u - K + 1 + j];  db = sum_u dpre[u].
 //
 // One thread owns 4 channels and walks kSub tokens and the K - 1 behind them (whose dpre reaches back into its tokens),
-// with a window of the last K inputs and of the last K dpre.  The forward pass is computed again on the way, so x, dy
-// are read and dx written once, apart from the K - 1 tokens at either end.  dw and db are summed per thread, over the
-// four warps of a block (adjacent tokens) and, by a second kernel, over the blocks, always in the same order.
-#include "common.cuh"
+// with a window of the last K inputs and of the last K dpre in registers.  The forward pass is computed again on the
+// way, so x and dy are read and dx written once, apart from the K - 1 tokens at either end, which the neighbouring warps
+// of the block read too.  Tokens come in batches of kBatch through a two-stage ring in shared memory (cp.async, every
+// thread its own places: no barrier), and a batch is unrolled so that the windows move by renaming registers.  dw and db
+// are summed per thread, over the four warps of a block (adjacent tokens) and, by a second kernel, over the blocks,
+// always in the same order.  Bound by HBM, with the issue slots next.
 #include "kernels.h"
+#include "pairs.cuh"
 
 namespace gdr {
 namespace {
 
-constexpr int kWarps = 4;            // warps of a block, adjacent in time
-constexpr int kSub = 64;             // tokens a warp walks
-constexpr int kTile = kWarps * kSub; // tokens of a block
-constexpr int V = 4;                 // channels of a thread
-
-template <typename T> __device__ __forceinline__ void load4(const T *p, float (&x)[V]);
-template <> __device__ __forceinline__ void load4<float>(const float *p, float (&x)[V]) {
-    const float4 f = *reinterpret_cast<const float4 *>(p);
-    x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
-}
-template <> __device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16 *p, float (&x)[V]) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
-    const float2 a = __bfloat1622float2(h[0]), b = __bfloat1622float2(h[1]);
-    x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
-}
-template <> __device__ __forceinline__ void load4<__half>(const __half *p, float (&x)[V]) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    const __half2 *h = reinterpret_cast<const __half2 *>(&u);
-    const float2 a = __half22float2(h[0]), b = __half22float2(h[1]);
-    x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
-}
-template <typename T> __device__ __forceinline__ void store4(T *p, const float (&x)[V]);
-template <> __device__ __forceinline__ void store4<float>(float *p, const float (&x)[V]) {
-    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
-}
-template <> __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16 *p, const float (&x)[V]) {
-    __nv_bfloat162 h[2] = {__floats2bfloat162_rn(x[0], x[1]), __floats2bfloat162_rn(x[2], x[3])};
-    *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<const uint2 *>(h);
-}
-template <> __device__ __forceinline__ void store4<__half>(__half *p, const float (&x)[V]) {
-    __half2 h[2] = {__floats2half2_rn(x[0], x[1]), __floats2half2_rn(x[2], x[3])};
-    *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<const uint2 *>(h);
-}
+constexpr int kWarps = 4;             // warps of a block, adjacent in time
+constexpr int kThreads = kWarps * 32;
+constexpr int kSub = 64;              // tokens a warp walks
+constexpr int kTile = kWarps * kSub;  // tokens of a block
+constexpr int kBatch = 8;             // tokens of a stage
+constexpr int V = 4;                  // channels of a thread
+constexpr int P = V / 2;
 
 // First element of channel group c0 of sequence b in dq, dk or dv (time 0), and that tensor's row length
 template <typename T>
@@ -63,105 +39,177 @@ __device__ __forceinline__ const T *dy_base(const ConvBwdArgs &a, int b, int c0,
     return static_cast<const T *>(a.dv) + ((size_t)b * a.Nv + c / a.Dv) * a.S * a.Dv + c % a.Dv;
 }
 
-// value of the history (state followed by x) at index i of sequence b, channel c: i < K from the state
-template <typename T, int K>
-__device__ __forceinline__ float hist_at(const ConvBwdArgs &a, int b, int c, int i) {
-    if (i < K) return a.state_in ? to_f32(static_cast<const T *>(a.state_in)[((size_t)b * a.C + c) * K + i]) : 0.f;
-    return to_f32(static_cast<const T *>(a.x)[((size_t)b * a.S + (i - K)) * a.C + c]);
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// silu'(p) = s (1 + p (1 - s)), s = 1 / (1 + e^{-p}): far left e^{-p} is infinite and s, and the whole, 0
+__device__ __forceinline__ float2 silu_slope(float2 p) {
+    float e0, e1, q0, q1;
+    up2(__fmul2_rn(p, both(-1.4426950408889634f)), e0, e1);
+    up2(__fadd2_rn(make_float2(ex2(e0), ex2(e1)), both(1.f)), q0, q1);
+    const float2 s = make_float2(rcp(q0), rcp(q1));
+    return __fmul2_rn(s, __ffma2_rn(p, __ffma2_rn(s, both(-1.f), both(1.f)), both(1.f)));
 }
 
+template <typename T> struct Stage {
+    RawV<T, V> x[2][kBatch][kThreads], dy[2][kBatch][kThreads];
+};
+
+// blocks of an SM that the registers are capped for: windows, taps and sums of 4 channels take 16 K + 8 of them
+template <typename T, int K> constexpr int kBlocks = K <= 4 ? 4 : 3;
+
 template <typename T, int K>
-__global__ void __launch_bounds__(kWarps * 32) conv1d_bwd_kernel(const ConvBwdArgs a) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__global__ void __launch_bounds__(kThreads, (kBlocks<T, K>)) conv1d_bwd_kernel(const ConvBwdArgs a) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    auto &sm = *reinterpret_cast<Stage<T> *>(smem);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int c0 = (blockIdx.x * 32 + lane) * V;
     const bool on = c0 < a.C;
     const int b = blockIdx.z;
     const int t0 = blockIdx.y * kTile + warp * kSub, t1 = min(t0 + kSub, a.S);
     const int Lr = a.lengths ? a.lengths[b] : a.S;
     const bool bad = Lr < 0 || Lr > a.S;
-    if (bad && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) raise_device_error(a.err, GDR_DEVERR_LENGTH);
+    if (bad && blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) raise_device_error(a.err, GDR_DEVERR_LENGTH);
     const int L = bad ? 0 : Lr;
 
-    float dw[K][V] = {}, db[V] = {};
+    float2 dw[K][P], db[P];
+    fill(db, 0.f);
+#pragma unroll
+    for (int j = 0; j < K; ++j) fill(dw[j], 0.f);
     const bool first = t0 == 0;  // also answers for the history before position 0
     if (on && (t0 < t1 || first)) {
         int row;
         const T *dy = dy_base<T>(a, b, c0, row);
         const T *x = static_cast<const T *>(a.x) + (size_t)b * a.S * a.C + c0;
         T *dx = static_cast<T *>(a.dx) + (size_t)b * a.S * a.C + c0;
-        const T *ds_out = a.dstate_out && !bad ? static_cast<const T *>(a.dstate_out) + ((size_t)b * a.C + c0) * K : nullptr;
-        T *ds_in = first && a.dstate_in ? static_cast<T *>(a.dstate_in) + ((size_t)b * a.C + c0) * K : nullptr;
-        float w[K][V], win[K][V], dwin[K][V], bias[V];
+        const size_t state = ((size_t)b * a.C + c0) * K;
+        const T *ds_out = a.dstate_out && !bad ? static_cast<const T *>(a.dstate_out) + state : nullptr;
+        T *ds_in = first && a.dstate_in ? static_cast<T *>(a.dstate_in) + state : nullptr;
+
+        const int end = t1 + K - 1;  // tokens t0 .. end - 1 are walked; those from L on count as zeros
+        auto fetch = [&](int u, int s) {
+            const int n = max(0, min(min(kBatch, end - u), L - u));
+            const size_t at = n > 0 ? (size_t)u : 0;
+            stage_segment<kBatch>(sm.x[s], x + at * a.C, (unsigned)a.C * (unsigned)sizeof(T), n);
+            stage_segment<kBatch>(sm.dy[s], dy + at * row, (unsigned)row * (unsigned)sizeof(T), n);
+            stage_commit();
+        };
+        fetch(t0, 0);
+        fetch(t0 + kBatch, 1);
+
+        float2 w[K][P], bias[P], win[K - 1 + kBatch][P], dwin[K - 1 + kBatch][P];
+        fill(bias, 0.f);
+        if (a.bias) unpack<T, V>(*reinterpret_cast<const RawV<T, V> *>(static_cast<const T *>(a.bias) + c0), bias);
+        {
+            alignas(16) T taps[V * K];  // the thread's rows of the weight are adjacent
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            bias[i] = a.bias ? to_f32(static_cast<const T *>(a.bias)[c0 + i]) : 0.f;
+            for (int j = 0; j < K; ++j)
+                reinterpret_cast<RawV<T, V> *>(taps)[j] =
+                    reinterpret_cast<const RawV<T, V> *>(static_cast<const T *>(a.w) + (size_t)c0 * K)[j];
 #pragma unroll
-            for (int j = 0; j < K; ++j) {
-                w[j][i] = to_f32(static_cast<const T *>(a.w)[(size_t)(c0 + i) * K + j]);
-                dwin[j][i] = 0.f;
-                // win[j] holds position u - K + 1 + j at step u: one short of it before the first step
-                win[j][i] = t0 < L && j > 0 ? hist_at<T, K>(a, b, c0 + i, t0 + j) : 0.f;
+            for (int j = 0; j < K; ++j)
+#pragma unroll
+                for (int i = 0; i < P; ++i) w[j][i] = make_float2(to_f32(taps[2 * i * K + j]), to_f32(taps[(2 * i + 1) * K + j]));
+        }
+        // win[j], j < K - 1: the inputs before the batch (position u - K + 1 + j at its first token u); dwin the same
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) {
+            fill(dwin[j], 0.f);
+            fill(win[j], 0.f);
+            const int at = t0 - K + 1 + j;
+            if (at >= 0) {
+                if (at < L) unpack<T, V>(*reinterpret_cast<const RawV<T, V> *>(x + (size_t)at * a.C), win[j]);
+            } else if (a.state_in && L > 0) {
+                const T *s = static_cast<const T *>(a.state_in) + state;
+#pragma unroll
+                for (int i = 0; i < P; ++i) win[j][i] = make_float2(to_f32(s[2 * i * K + at + K]), to_f32(s[(2 * i + 1) * K + at + K]));
             }
         }
         // the oldest history entry is no input of the conv; it is passed on where the sequence is empty
         if (ds_in)
 #pragma unroll
             for (int i = 0; i < V; ++i) ds_in[i * K] = from_f32<T>(ds_out && L == 0 ? to_f32(ds_out[i * K]) : 0.f);
-        for (int u = t0; u < t1 + K - 1; ++u) {
+
+        // token u, at place j of the windows, its inputs at place p of stage s; whole: an ordinary one of the thread's tokens
+        auto step = [&](int u, int j, int s, int p, bool whole) {
+            float2 g[P];
+            unpack<T, V>(sm.x[s][p][tid], win[K - 1 + j]);
+            unpack<T, V>(sm.dy[s][p][tid], g);
 #pragma unroll
-            for (int j = 0; j < K - 1; ++j)
+            for (int i = 0; i < P; ++i) {
+                float2 pre = bias[i];
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    win[j][i] = win[j + 1][i];
-                    dwin[j][i] = dwin[j + 1][i];
-                }
+                for (int q = 0; q < K; ++q) pre = __ffma2_rn(w[q][i], win[j + q][i], pre);
+                const float2 d = __fmul2_rn(g[i], silu_slope(pre));
+                dwin[K - 1 + j][i] = d;
+                if (whole || u < t1) {
+                    db[i] = __fadd2_rn(db[i], d);
 #pragma unroll
-            for (int i = 0; i < V; ++i) dwin[K - 1][i] = 0.f;
-            if (u < L) {
-                float g[V];
-                load4(x + (size_t)u * a.C, win[K - 1]);
-                load4(dy + (size_t)u * row, g);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    float p = bias[i];
-#pragma unroll
-                    for (int j = 0; j < K; ++j) p = fmaf(w[j][i], win[j][i], p);
-                    const float s = 1.f / (1.f + expf(-p));
-                    const float d = g[i] * (s * fmaf(p, 1.f - s, 1.f));
-                    dwin[K - 1][i] = d;
-                    if (u < t1) {
-                        db[i] += d;
-#pragma unroll
-                        for (int j = 0; j < K; ++j) dw[j][i] = fmaf(d, win[j][i], dw[j][i]);
-                    }
+                    for (int q = 0; q < K; ++q) dw[q][i] = __ffma2_rn(d, win[j + q][i], dw[q][i]);
                 }
             }
             const int t = u - K + 1;  // its last dpre has arrived
-            float r[V];
+            float2 r[P];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                r[i] = 0.f;
+            for (int i = 0; i < P; ++i) {
+                r[i] = __fmul2_rn(w[0][i], dwin[j + K - 1][i]);
 #pragma unroll
-                for (int j = 0; j < K; ++j) r[i] = fmaf(w[j][i], dwin[K - 1 - j][i], r[i]);
-                // the new state is the history from place L on: place j of it is position L - K + j
-                if (ds_out && t >= L - K && t < L) r[i] += to_f32(ds_out[i * K + t - L + K]);
+                for (int q = 1; q < K; ++q) r[i] = __ffma2_rn(w[q][i], dwin[j + K - 1 - q][i], r[i]);
             }
-            if (t >= t0) {
-                if (t >= L)
+            if (!whole && ds_out && t >= L - K && t < L) {
+                // the new state is the history from place L on: place q of it is position L - K + q
 #pragma unroll
-                    for (int i = 0; i < V; ++i) r[i] = 0.f;
-                store4(dx + (size_t)t * a.C, r);
-            } else if (ds_in) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) ds_in[i * K + t + K] = from_f32<T>(r[i]);
+                for (int i = 0; i < P; ++i)
+                    r[i] = __fadd2_rn(r[i], make_float2(to_f32(ds_out[2 * i * K + t - L + K]), to_f32(ds_out[(2 * i + 1) * K + t - L + K])));
             }
+            if ((whole && j >= K - 1) || t >= t0) {
+                store<T, V>(dx + (size_t)t * a.C, r);
+            } else if (!whole && ds_in) {
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    float lo, hi;
+                    up2(r[i], lo, hi);
+                    ds_in[2 * i * K + t + K] = from_f32<T>(lo);
+                    ds_in[(2 * i + 1) * K + t + K] = from_f32<T>(hi);
+                }
+            }
+        };
+        auto shift = [&](int by) {
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    win[j][i] = win[by + j][i];
+                    dwin[j][i] = dwin[by + j][i];
+                }
+        };
+        int s = 0;
+#pragma unroll 1
+        for (int u = t0; u < end; u += kBatch, s ^= 1) {
+            stage_wait_but_one();
+            // every token of the batch is one of the thread's, and none that it completes lies before the sequence or
+            // takes part in the new state
+            if ((u > t0 || !first) && u + kBatch <= t1 && (!ds_out || u + kBatch < L)) {
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) step(u + j, j, s, j, true);
+                shift(kBatch);
+            } else {
+#pragma unroll 1
+                for (int j = 0; j < kBatch && u + j < end; ++j) {
+                    step(u + j, 0, s, j, false);
+                    shift(1);
+                }
+            }
+            fetch(u + 2 * kBatch, s);
         }
     }
     if (!a.partial) return;
-    __shared__ float part[kWarps - 1][K + 1][V][32];
+    __shared__ float2 part[kWarps - 1][K + 1][P][32];
     if (warp > 0)
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+        for (int i = 0; i < P; ++i) {
 #pragma unroll
             for (int j = 0; j < K; ++j) part[warp - 1][j][i][lane] = dw[j][i];
             part[warp - 1][K][i][lane] = db[i];
@@ -171,14 +219,14 @@ __global__ void __launch_bounds__(kWarps * 32) conv1d_bwd_kernel(const ConvBwdAr
         float *p = a.partial + ((size_t)(b * gridDim.y + blockIdx.y) * (K + 1)) * a.C + c0;
 #pragma unroll
         for (int j = 0; j <= K; ++j) {
-            float r[V];
+            float2 r[P];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
+            for (int i = 0; i < P; ++i) {
                 r[i] = j < K ? dw[j < K ? j : 0][i] : db[i];
 #pragma unroll
-                for (int q = 0; q < kWarps - 1; ++q) r[i] += part[q][j][i][lane];
+                for (int q = 0; q < kWarps - 1; ++q) r[i] = __fadd2_rn(r[i], part[q][j][i][lane]);
             }
-            store4(p + (size_t)j * a.C, r);
+            store<float, V>(p + (size_t)j * a.C, r);
         }
     }
 }
@@ -211,10 +259,14 @@ int tiles(int S) { return (S + kTile - 1) / kTile; }
 
 template <typename T, int K>
 cudaError_t launch_tk(const ConvBwdArgs &a, cudaStream_t s) {
+    static LaunchCache cache(reinterpret_cast<const void *>(conv1d_bwd_kernel<T, K>));
+    const int smem = (int)sizeof(Stage<T>);
+    cudaError_t e = cache.allow_smem(smem);
+    if (e != cudaSuccess) return e;
     const unsigned gx = (unsigned)((a.C + 32 * V - 1) / (32 * V));
     const unsigned gy = (unsigned)(a.S > 0 ? tiles(a.S) : 1);  // without tokens, the state's gradient alone
-    conv1d_bwd_kernel<T, K><<<dim3(gx, gy, a.B), kWarps * 32, 0, s>>>(a);
-    cudaError_t e = cudaGetLastError();
+    conv1d_bwd_kernel<T, K><<<dim3(gx, gy, a.B), kThreads, smem, s>>>(a);
+    e = cudaGetLastError();
     if (e != cudaSuccess || !a.partial) return e;
     conv1d_bwd_sum_kernel<<<dim3((unsigned)((a.C + 31) / 32), K + 1), 1024, 0, s>>>(a.partial, (int)(a.B * gy), a.C, K,
                                                                                  a.dw, a.db);

@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(kThreads, (kBlocksOf<T, kMix>)) scan_bwd_kerne
     const int c0 = (slab * lx + cl) * V;
     const bool on = c0 < a.D;
     const int Lr = seq_len(a.lengths, (int)(bn / a.N), a.S);
-    const int L = Lr < 0 ? 0 : Lr;
+    const unsigned L = Lr < 0 ? 0u : (unsigned)Lr, S = (unsigned)a.S;
     if (Lr < 0 && tid == 0 && rank == 0) raise_device_error(a.err, GDR_DEVERR_LENGTH);
 
     const unsigned row_x = (unsigned)a.D * sizeof(T), row_g = (unsigned)a.D * sizeof(G);
@@ -54,12 +54,12 @@ __global__ void __launch_bounds__(kThreads, (kBlocksOf<T, kMix>)) scan_bwd_kerne
     char *dg = reinterpret_cast<char *>(static_cast<G *>(a.dg) + base);
     const int chunks = (a.S + kChunk - 1) / kChunk;
     const float *ck = a.checkpoints + (size_t)bn * chunks * a.D + c0;
-    f2_t mu[P];  // what the tokens behind the cluster's tiles pass back, the same in every block
+    float2 mu[P];  // what the tokens behind the cluster's tiles pass back, the same in every block
     fill(mu, 0.f);
     if (on && a.dfinal_state && Lr >= 0) load_f32<V>(a.dfinal_state + (size_t)bn * a.D + c0, mu);
 
     const int TT = kSteps * (kThreads / lx);
-    const long long step = (long long)R * TT;
+    const unsigned step = (unsigned)R * TT;  // counted without sign: tiles may end past 2^31
     const int tiles = (int)((L + step - 1) / step);
     constexpr int kSegs = kChunk / kSteps;  // segments of a chunk
     const int chunk_warps = kSegs * lx > 32 ? kSegs * lx / 32 : 1;  // warps of a chunk: no warp holds more than one
@@ -74,32 +74,24 @@ __global__ void __launch_bounds__(kThreads, (kBlocksOf<T, kMix>)) scan_bwd_kerne
         cluster_meet();
     }
 
-    // rows of whole 16 bytes are staged by the warp (stage_rows)
-    const bool by_warp = kWide && (a.D & 7) == 0;
-    const long long left = ((long long)a.D - slab * 32 * V) * 2;  // bytes of a row of 16-bit elements from the slab on
+    const int left = kWide ? (a.D - slab * 32 * V) * 2 : 0;  // bytes of a row of 16-bit elements from the slab on
     auto fetch = [&](int k) {
-        const long long t0 = k * step + (long long)rank * TT + seg * kSteps;
-        const int nt = (int)max(0LL, min((long long)kSteps, L - t0)), n = on ? nt : 0;
-        const size_t at = nt > 0 ? (size_t)t0 : 0;
-        if constexpr (kWide && sizeof(G) * V == 8) {
-            if (by_warp) stage_rows<kSteps>(sm.g, g + at * row_g - lane * 8, row_g, nt, left);
-            else stage_segment<kSteps>(sm.g, g + at * row_g, row_g, n);
-        } else {
-            stage_segment<kSteps>(sm.g, g + at * row_g, row_g, n);
-        }
-        if constexpr (kWide && sizeof(T) * V == 8) {
-            if (by_warp) stage_rows<kSteps>(sm.x, x + at * row_x - lane * 8, row_x, nt, left);
-            else stage_segment<kSteps>(sm.x, x + at * row_x, row_x, n);
-        } else {
-            stage_segment<kSteps>(sm.x, x + at * row_x, row_x, n);
-        }
-        if constexpr (kWide && sizeof(T) * V == 8) {
-            if (by_warp) stage_rows<kSteps>(sm.d, d + at * row_x - lane * 8, row_x, nt, left);
-            else stage_segment<kSteps>(sm.d, d + at * row_x, row_x, n);
-        } else {
-            stage_segment<kSteps>(sm.d, d + at * row_x, row_x, n);
-        }
-        const long long chunk = t0 / kChunk;
+        const unsigned t0 = k * step + rank * TT + seg * kSteps;
+        const int nt = t0 < L ? (int)min((unsigned)kSteps, L - t0) : 0;
+        const size_t at = nt > 0 ? t0 : 0;
+        if constexpr (kWide && sizeof(G) * V == 8)
+            stage_rows<kSteps>(sm.g, g + at * row_g - lane * 8, row_g, nt, left);
+        else
+            stage_segment<kSteps>(sm.g, g + at * row_g, row_g, on ? nt : 0);
+        if constexpr (kWide && sizeof(T) * V == 8)
+            stage_rows<kSteps>(sm.x, x + at * row_x - lane * 8, row_x, nt, left);
+        else
+            stage_segment<kSteps>(sm.x, x + at * row_x, row_x, on ? nt : 0);
+        if constexpr (kWide && sizeof(T) * V == 8)
+            stage_rows<kSteps>(sm.d, d + at * row_x - lane * 8, row_x, nt, left);
+        else
+            stage_segment<kSteps>(sm.d, d + at * row_x, row_x, on ? nt : 0);
+        const unsigned chunk = t0 / kChunk;
         const bool has = on && chunk * kChunk < L;
         stage<RawV<float, V>, true>(&sm.h[tid], ck + (has ? (size_t)chunk * a.D : 0), has);
         stage_commit();
@@ -107,58 +99,58 @@ __global__ void __launch_bounds__(kThreads, (kBlocksOf<T, kMix>)) scan_bwd_kerne
     if (tiles > 0) fetch(tiles - 1);
     for (int k = tiles - 1, n = 0; k >= 0; --k, ++n) {
         const int p = n & 1;
-        const long long t0 = k * step + (long long)rank * TT + seg * kSteps;
+        const unsigned t0 = k * step + rank * TT + seg * kSteps;
         // a segment forwards, (A, F): h -> A h + F, and backwards, (A, B): mu -> A mu + B; behind the sequence a = 1 and
         // x = dout = 0, which changes neither
-        f2_t av[kSteps][P], rest[kMix ? kSteps : 1][P], xv[kSteps][P], A[P], F[P], B[P];
+        float2 av[kSteps][P], rest[kMix ? kSteps : 1][P], xv[kSteps][P], A[P], F[P], B[P];
         RawV<T, V> dr[kSteps];
         stage_wait();
         if (kWide) __syncwarp();
-        f2_t h[P];
+        float2 h[P];
         unpack<float, V>(sm.h[tid], h);
 #pragma unroll
         for (int j = 0; j < kSteps; ++j) {
-            f2_t gv[P];
+            float2 gv[P];
             unpack<G, V>(sm.g[j][tid], gv);
             unpack<T, V>(sm.x[j][tid], xv[j]);
             dr[j] = sm.d[j][tid];
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                f2_t r;
+                float2 r;
                 decay<kMix>(gv[i], av[j][i], r);
                 if (kMix) rest[kMix ? j : 0][i] = r;
-                const f2_t b = kMix ? mul2(xv[j][i], r) : xv[j][i];
-                A[i] = j ? mul2(A[i], av[j][i]) : av[j][i];
-                F[i] = j ? fma2(av[j][i], F[i], b) : b;
+                const float2 b = kMix ? __fmul2_rn(xv[j][i], r) : xv[j][i];
+                A[i] = j ? __fmul2_rn(A[i], av[j][i]) : av[j][i];
+                F[i] = j ? __ffma2_rn(av[j][i], F[i], b) : b;
             }
         }
 #pragma unroll
         for (int j = kSteps - 1; j >= 0; --j) {
-            f2_t dv[P];
+            float2 dv[P];
             unpack<T, V>(dr[j], dv);
 #pragma unroll
-            for (int i = 0; i < P; ++i) B[i] = mul2(av[j][i], j < kSteps - 1 ? add2(dv[i], B[i]) : dv[i]);
+            for (int i = 0; i < P; ++i) B[i] = __fmul2_rn(av[j][i], j < kSteps - 1 ? __fadd2_rn(dv[i], B[i]) : dv[i]);
         }
         if (kWide) __syncwarp();
         if (k > 0) fetch(k - 1);  // what this thread (this warp) copied for itself is in registers
         // over the segments of the warp: (EA, EF) those before this one, (LA, LB) those behind it
-        f2_t EA[P], EF[P], LA[P], LB[P];
+        float2 EA[P], EF[P], LA[P], LB[P];
         if constexpr (!kWide) {
-            f2_t TA[P];
+            float2 TA[P];
 #pragma unroll
             for (int i = 0; i < P; ++i) TA[i] = LA[i] = A[i];
             for (int q = lx; q < 32; q *= 2) {
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
-                    const f2_t pa = shfl_up2(TA[i], q), pf = shfl_up2(F[i], q);
+                    const float2 pa = shfl_up2(TA[i], q), pf = shfl_up2(F[i], q);
                     if (lane >= q) {
-                        F[i] = fma2(TA[i], pf, F[i]);
-                        TA[i] = mul2(TA[i], pa);
+                        F[i] = __ffma2_rn(TA[i], pf, F[i]);
+                        TA[i] = __fmul2_rn(TA[i], pa);
                     }
-                    const f2_t na = shfl_down2(LA[i], q), nb = shfl_down2(B[i], q);
+                    const float2 na = shfl_down2(LA[i], q), nb = shfl_down2(B[i], q);
                     if (lane + q < 32) {
-                        B[i] = fma2(LA[i], nb, B[i]);
-                        LA[i] = mul2(LA[i], na);
+                        B[i] = __ffma2_rn(LA[i], nb, B[i]);
+                        LA[i] = __fmul2_rn(LA[i], na);
                     }
                 }
             }
@@ -183,18 +175,18 @@ __global__ void __launch_bounds__(kThreads, (kBlocksOf<T, kMix>)) scan_bwd_kerne
         if (R > 1) {  // as in the forward kernel, the block's backward map to every block of the cluster
             if (tid == 0) sm100::mbar_arrive_expect_tx(&sm.arrived[p], exchange);
             if (warp < R && lane < lx) {
-                f2_t ta[P], tb[P];
+                float2 ta[P], tb[P];
                 load_f32<V>(&sm.wa[p][kWarps - 1][cl * V], ta);
                 load_f32<V>(&sm.wr[p][kWarps - 1][cl * V], tb);
 #pragma unroll
                 for (int w = kWarps - 2; w >= 0; --w) {
-                    f2_t wa[P], wb[P];
+                    float2 wa[P], wb[P];
                     load_f32<V>(&sm.wa[p][w][cl * V], wa);
                     load_f32<V>(&sm.wr[p][w][cl * V], wb);
 #pragma unroll
                     for (int i = 0; i < P; ++i) {
-                        tb[i] = fma2(wa[i], tb[i], wb[i]);
-                        ta[i] = mul2(ta[i], wa[i]);
+                        tb[i] = __ffma2_rn(wa[i], tb[i], wb[i]);
+                        ta[i] = __fmul2_rn(ta[i], wa[i]);
                     }
                 }
                 put_remote<V>(&sm.ca[p][rank][cl * V], &sm.arrived[p], warp, ta);
@@ -204,23 +196,23 @@ __global__ void __launch_bounds__(kThreads, (kBlocksOf<T, kMix>)) scan_bwd_kerne
         }
         // the state before the segment: the chunk's checkpoint, the chunk's warps before this one, its segments
         for (int w = warp & ~(chunk_warps - 1); w < warp; ++w) {
-            f2_t wa[P], wf[P];
+            float2 wa[P], wf[P];
             load_f32<V>(&sm.wa[p][w][cl * V], wa);
             load_f32<V>(&sm.wf[p][w][cl * V], wf);
 #pragma unroll
-            for (int i = 0; i < P; ++i) h[i] = fma2(wa[i], h[i], wf[i]);
+            for (int i = 0; i < P; ++i) h[i] = __ffma2_rn(wa[i], h[i], wf[i]);
         }
         if (!kWide && lane >= lx) {
 #pragma unroll
-            for (int i = 0; i < P; ++i) h[i] = fma2(EA[i], h[i], EF[i]);
+            for (int i = 0; i < P; ++i) h[i] = __ffma2_rn(EA[i], h[i], EF[i]);
         }
         // every token's h_{t-1} (less x_t) in the place of its x
 #pragma unroll
         for (int j = 0; j < kSteps; ++j)
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                const f2_t q = kMix ? fma2(xv[j][i], both(-1.f), h[i]) : h[i];
-                h[i] = kMix ? fma2(av[j][i], h[i], mul2(xv[j][i], rest[kMix ? j : 0][i])) : fma2(av[j][i], h[i], xv[j][i]);
+                const float2 q = kMix ? __ffma2_rn(xv[j][i], both(-1.f), h[i]) : h[i];
+                h[i] = kMix ? __ffma2_rn(av[j][i], h[i], __fmul2_rn(xv[j][i], rest[kMix ? j : 0][i])) : __ffma2_rn(av[j][i], h[i], xv[j][i]);
                 xv[j][i] = q;
             }
         if (R > 1 && !lost && !wait_remote(&sm.arrived[p], (unsigned)(n >> 1) & 1u, a.wait_ns)) {
@@ -228,18 +220,18 @@ __global__ void __launch_bounds__(kThreads, (kBlocksOf<T, kMix>)) scan_bwd_kerne
             raise_device_error(a.err, GDR_DEVERR_TIMEOUT);
         }
         // what comes back to this segment: from behind the tiles, the later blocks, the later warps, the later segments
-        f2_t m[P];
+        float2 m[P];
         if (R > 1) {
             for (int r = R - 1; r >= 0; --r) {
                 if (r == rank) {
 #pragma unroll
                     for (int i = 0; i < P; ++i) m[i] = mu[i];
                 }
-                f2_t ra[P], rb[P];
+                float2 ra[P], rb[P];
                 load_f32<V>(&sm.ca[p][r][cl * V], ra);
                 load_f32<V>(&sm.cr[p][r][cl * V], rb);
 #pragma unroll
-                for (int i = 0; i < P; ++i) mu[i] = fma2(ra[i], mu[i], rb[i]);
+                for (int i = 0; i < P; ++i) mu[i] = __ffma2_rn(ra[i], mu[i], rb[i]);
             }
         } else {
 #pragma unroll
@@ -248,11 +240,11 @@ __global__ void __launch_bounds__(kThreads, (kBlocksOf<T, kMix>)) scan_bwd_kerne
 #pragma unroll
         for (int w = kWarps - 1; w > 0; --w) {
             if (w <= warp) break;
-            f2_t wa[P], wb[P];
+            float2 wa[P], wb[P];
             load_f32<V>(&sm.wa[p][w][cl * V], wa);
             load_f32<V>(&sm.wr[p][w][cl * V], wb);
 #pragma unroll
-            for (int i = 0; i < P; ++i) m[i] = fma2(wa[i], m[i], wb[i]);
+            for (int i = 0; i < P; ++i) m[i] = __ffma2_rn(wa[i], m[i], wb[i]);
         }
         if (R == 1) {  // the whole tile: on through this warp and the earlier ones
 #pragma unroll
@@ -260,33 +252,33 @@ __global__ void __launch_bounds__(kThreads, (kBlocksOf<T, kMix>)) scan_bwd_kerne
 #pragma unroll
             for (int w = kWarps - 1; w >= 0; --w) {
                 if (w > warp) continue;
-                f2_t wa[P], wb[P];
+                float2 wa[P], wb[P];
                 load_f32<V>(&sm.wa[p][w][cl * V], wa);
                 load_f32<V>(&sm.wr[p][w][cl * V], wb);
 #pragma unroll
-                for (int i = 0; i < P; ++i) mu[i] = fma2(wa[i], mu[i], wb[i]);
+                for (int i = 0; i < P; ++i) mu[i] = __ffma2_rn(wa[i], mu[i], wb[i]);
             }
         }
         if (!kWide && lane + lx < 32) {
 #pragma unroll
-            for (int i = 0; i < P; ++i) m[i] = fma2(LA[i], m[i], LB[i]);
+            for (int i = 0; i < P; ++i) m[i] = __ffma2_rn(LA[i], m[i], LB[i]);
         }
         char *ox = dx + (size_t)t0 * row_x, *og = dg + (size_t)t0 * row_g;
-        auto back = [&](int j, f2_t (&rx)[P], f2_t (&rg)[P]) {
-            f2_t dv[P];
+        auto back = [&](int j, float2 (&rx)[P], float2 (&rg)[P]) {
+            float2 dv[P];
             unpack<T, V>(dr[j], dv);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                const f2_t lam = add2(dv[i], m[i]);
-                m[i] = mul2(av[j][i], lam);
-                rx[i] = kMix ? mul2(rest[kMix ? j : 0][i], lam) : lam;
-                rg[i] = mul2(m[i], xv[j][i]);
+                const float2 lam = __fadd2_rn(dv[i], m[i]);
+                m[i] = __fmul2_rn(av[j][i], lam);
+                rx[i] = kMix ? __fmul2_rn(rest[kMix ? j : 0][i], lam) : lam;
+                rg[i] = __fmul2_rn(m[i], xv[j][i]);
             }
         };
         if (on && t0 + kSteps <= L) {
 #pragma unroll
             for (int j = kSteps - 1; j >= 0; --j) {
-                f2_t rx[P], rg[P];
+                float2 rx[P], rg[P];
                 back(j, rx, rg);
                 store<T, V>(ox + j * (size_t)row_x, rx);
                 store<G, V>(og + j * (size_t)row_g, rg);
@@ -294,13 +286,13 @@ __global__ void __launch_bounds__(kThreads, (kBlocksOf<T, kMix>)) scan_bwd_kerne
         } else if (on) {
 #pragma unroll
             for (int j = kSteps - 1; j >= 0; --j) {
-                f2_t rx[P], rg[P];
+                float2 rx[P], rg[P];
                 back(j, rx, rg);
                 if (t0 + j >= L) {
                     fill(rx, 0.f);
                     fill(rg, 0.f);
                 }
-                if (t0 + j < a.S) {
+                if (t0 + j < S) {
                     store<T, V>(ox + j * (size_t)row_x, rx);
                     store<G, V>(og + j * (size_t)row_g, rg);
                 }
@@ -309,9 +301,9 @@ __global__ void __launch_bounds__(kThreads, (kBlocksOf<T, kMix>)) scan_bwd_kerne
     }
     if (R > 1) cluster_meet();  // a block that gave up must not leave while the others write to it
     if (!on) return;
-    f2_t zero[P];
+    float2 zero[P];
     fill(zero, 0.f);
-    for (long long t = tiles * step + (long long)rank * (kThreads / lx) + seg; t < a.S; t += (long long)R * (kThreads / lx)) {
+    for (unsigned t = tiles * step + rank * (kThreads / lx) + seg; t < S; t += R * (kThreads / lx)) {
         store<T, V>(dx + (size_t)t * row_x, zero);
         store<G, V>(dg + (size_t)t * row_g, zero);
     }
@@ -334,7 +326,7 @@ template <typename T, typename G, bool kMix> cudaError_t launch_m(const ScanBwdA
     const long long rows = (long long)a.B * a.N;
     const int blocks = kBlocksOf<T, kMix> * sm_count();
     if (a.D % 4 == 0) {
-        const Cut cut = choose_cut(rows, a.D, 4, a.S, kSteps, kCanBeWide ? 32 : 16, kMin, blocks);
+        const Cut cut = choose_cut(rows, a.D, 4, a.S, kSteps, kCanBeWide && wide_rows<T>(a.D) ? 32 : 16, kMin, blocks);
         if constexpr (kCanBeWide)
             if (cut.lx == 32) return launch_v<T, G, kMix, 4, true>(a, cut, s);
         return launch_v<T, G, kMix, 4, false>(a, cut, s);

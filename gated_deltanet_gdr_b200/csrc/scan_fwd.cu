@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
     const int c0 = (slab * lx + cl) * V;
     const bool on = c0 < a.D;
     const int Lr = seq_len(a.lengths, (int)(bn / a.N), a.S);
-    const int L = Lr < 0 ? 0 : Lr;
+    const unsigned L = Lr < 0 ? 0u : (unsigned)Lr, S = (unsigned)a.S;
     if (Lr < 0 && tid == 0 && rank == 0) raise_device_error(a.err, GDR_DEVERR_LENGTH);
 
     constexpr int P = kPairs<V>;
@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
     const char *x = reinterpret_cast<const char *>(static_cast<const T *>(a.x) + base);
     const char *g = reinterpret_cast<const char *>(static_cast<const G *>(a.g) + base);
     char *out = reinterpret_cast<char *>(static_cast<T *>(a.out) + base);
-    f2_t h[P];  // the state at the start of the cluster's next tiles, the same in every block
+    float2 h[P];  // the state at the start of the cluster's next tiles, the same in every block
     fill(h, 0.f);
     if (on && a.initial_state) load_f32<V>(a.initial_state + (size_t)bn * a.D + c0, h);
     const int chunks = (a.S + kChunk - 1) / kChunk;
@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
     if (L == 0 && Lr == 0 && ck && on && seg == 0 && rank == 0 && a.S > 0) store<float, V>(ck, h);
 
     const int TT = kSteps * (kThreads / lx);
-    const long long step = (long long)R * TT;  // tokens of the cluster's tiles
+    const unsigned step = (unsigned)R * TT;  // tokens of the cluster's tiles; counted without sign, they may end past 2^31
     const int tiles = (int)((L + step - 1) / step);
     const unsigned exchange = (unsigned)(R * lx * V * 2 * sizeof(float));  // bytes of a tile's (A, B) of all blocks
     bool lost = false;  // a wait ran out: no further waits
@@ -66,69 +66,63 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
         cluster_meet();  // every block of the cluster has started, with its barriers ready
     }
 
-    // rows of whole 16 bytes are staged by the warp (stage_rows)
-    const bool by_warp = kWide && (a.D & 7) == 0;
-    const long long left = ((long long)a.D - slab * 32 * V) * 2;  // bytes of a row of 16-bit elements from the slab on
+    const int left = kWide ? (a.D - slab * 32 * V) * 2 : 0;  // bytes of a row of 16-bit elements from the slab on
     auto fetch = [&](int k) {
-        const long long t0 = k * step + (long long)rank * TT + seg * kSteps;
-        const int nt = (int)max(0LL, min((long long)kSteps, L - t0)), n = on ? nt : 0;
-        const size_t at = nt > 0 ? (size_t)t0 : 0;
-        if constexpr (kWide && sizeof(G) * V == 8) {
-            if (by_warp) stage_rows<kSteps>(sm.g, g + at * row_g - lane * 8, row_g, nt, left);
-            else stage_segment<kSteps>(sm.g, g + at * row_g, row_g, n);
-        } else {
-            stage_segment<kSteps>(sm.g, g + at * row_g, row_g, n);
-        }
-        if constexpr (kWide && sizeof(T) * V == 8) {
-            if (by_warp) stage_rows<kSteps>(sm.x, x + at * row_x - lane * 8, row_x, nt, left);
-            else stage_segment<kSteps>(sm.x, x + at * row_x, row_x, n);
-        } else {
-            stage_segment<kSteps>(sm.x, x + at * row_x, row_x, n);
-        }
+        const unsigned t0 = k * step + rank * TT + seg * kSteps;
+        const int nt = t0 < L ? (int)min((unsigned)kSteps, L - t0) : 0;
+        const size_t at = nt > 0 ? t0 : 0;
+        if constexpr (kWide && sizeof(G) * V == 8)
+            stage_rows<kSteps>(sm.g, g + at * row_g - lane * 8, row_g, nt, left);
+        else
+            stage_segment<kSteps>(sm.g, g + at * row_g, row_g, on ? nt : 0);
+        if constexpr (kWide && sizeof(T) * V == 8)
+            stage_rows<kSteps>(sm.x, x + at * row_x - lane * 8, row_x, nt, left);
+        else
+            stage_segment<kSteps>(sm.x, x + at * row_x, row_x, on ? nt : 0);
         stage_commit();
     };
     if (tiles > 0) fetch(0);
     for (int k = 0; k < tiles; ++k) {
         const int p = k & 1;
-        const long long t0 = k * step + (long long)rank * TT + seg * kSteps;
+        const unsigned t0 = k * step + rank * TT + seg * kSteps;
         // decays and writes of the segment (tokens behind the sequence: a = 1, b = 0), and the segment as a whole
-        f2_t av[kSteps][P], bv[kSteps][P], A[P], B[P];
+        float2 av[kSteps][P], bv[kSteps][P], A[P], B[P];
         stage_wait();
         if (kWide) __syncwarp();
 #pragma unroll
         for (int j = 0; j < kSteps; ++j) {
-            f2_t gv[P];
+            float2 gv[P];
             unpack<G, V>(sm.g[j][tid], gv);
             unpack<T, V>(sm.x[j][tid], bv[j]);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                f2_t rest;
+                float2 rest;
                 decay<kMix>(gv[i], av[j][i], rest);
-                if (kMix) bv[j][i] = mul2(bv[j][i], rest);
-                A[i] = j ? mul2(A[i], av[j][i]) : av[j][i];
-                B[i] = j ? fma2(av[j][i], B[i], bv[j][i]) : bv[j][i];
+                if (kMix) bv[j][i] = __fmul2_rn(bv[j][i], rest);
+                A[i] = j ? __fmul2_rn(A[i], av[j][i]) : av[j][i];
+                B[i] = j ? __ffma2_rn(av[j][i], B[i], bv[j][i]) : bv[j][i];
             }
         }
         if (kWide) __syncwarp();
         if (k + 1 < tiles) fetch(k + 1);  // what this thread (this warp) copied for itself is in registers
         // inclusive composition over the segments of the warp; (EA, EB): the segments before this one
-        f2_t EA[P], EB[P];
+        float2 EA[P], EB[P];
         fill(EA, 1.f);
         fill(EB, 0.f);
         if (!kWide) {
             for (int d = lx; d < 32; d *= 2) {
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
-                    const f2_t pa = shfl_up2(A[i], d), pb = shfl_up2(B[i], d);
+                    const float2 pa = shfl_up2(A[i], d), pb = shfl_up2(B[i], d);
                     if (lane >= d) {
-                        B[i] = fma2(A[i], pb, B[i]);
-                        A[i] = mul2(A[i], pa);
+                        B[i] = __ffma2_rn(A[i], pb, B[i]);
+                        A[i] = __fmul2_rn(A[i], pa);
                     }
                 }
             }
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                const f2_t pa = shfl_up2(A[i], lx), pb = shfl_up2(B[i], lx);
+                const float2 pa = shfl_up2(A[i], lx), pb = shfl_up2(B[i], lx);
                 if (lane >= lx) {
                     EA[i] = pa;
                     EB[i] = pb;
@@ -145,18 +139,18 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
             // tiles on, having received the tile between, which its owner sent after reading this one.
             if (tid == 0) sm100::mbar_arrive_expect_tx(&sm.arrived[p], exchange);
             if (warp < R && lane < lx) {
-                f2_t ta[P], tb[P];
+                float2 ta[P], tb[P];
                 load_f32<V>(&sm.wa[p][0][cl * V], ta);
                 load_f32<V>(&sm.wb[p][0][cl * V], tb);
 #pragma unroll
                 for (int w = 1; w < kWarps; ++w) {
-                    f2_t wa[P], wb[P];
+                    float2 wa[P], wb[P];
                     load_f32<V>(&sm.wa[p][w][cl * V], wa);
                     load_f32<V>(&sm.wb[p][w][cl * V], wb);
 #pragma unroll
                     for (int i = 0; i < P; ++i) {
-                        tb[i] = fma2(wa[i], tb[i], wb[i]);
-                        ta[i] = mul2(ta[i], wa[i]);
+                        tb[i] = __ffma2_rn(wa[i], tb[i], wb[i]);
+                        ta[i] = __fmul2_rn(ta[i], wa[i]);
                     }
                 }
                 put_remote<V>(&sm.ca[p][rank][cl * V], &sm.arrived[p], warp, ta);
@@ -169,40 +163,40 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
             }
         }
         // the state this thread starts from: the tile's start, the blocks and warps before it, its warp's segments
-        f2_t hs[P];
+        float2 hs[P];
 #pragma unroll
         for (int i = 0; i < P; ++i) hs[i] = h[i];
         for (int r = 0; r < (R > 1 ? R : 0); ++r) {
-            f2_t ra[P], rb[P];
+            float2 ra[P], rb[P];
             load_f32<V>(&sm.ca[p][r][cl * V], ra);
             load_f32<V>(&sm.cb[p][r][cl * V], rb);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                h[i] = fma2(ra[i], h[i], rb[i]);
+                h[i] = __ffma2_rn(ra[i], h[i], rb[i]);
                 if (r < rank) hs[i] = h[i];
             }
         }
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             if (R > 1 && w >= warp) break;
-            f2_t wa[P], wb[P];
+            float2 wa[P], wb[P];
             load_f32<V>(&sm.wa[p][w][cl * V], wa);
             load_f32<V>(&sm.wb[p][w][cl * V], wb);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 if (R > 1) {
-                    hs[i] = fma2(wa[i], hs[i], wb[i]);
+                    hs[i] = __ffma2_rn(wa[i], hs[i], wb[i]);
                 } else {
-                    h[i] = fma2(wa[i], h[i], wb[i]);
+                    h[i] = __ffma2_rn(wa[i], h[i], wb[i]);
                     if (w < warp) hs[i] = h[i];
                 }
             }
         }
         if (!kWide) {
 #pragma unroll
-            for (int i = 0; i < P; ++i) hs[i] = fma2(EA[i], hs[i], EB[i]);
+            for (int i = 0; i < P; ++i) hs[i] = __ffma2_rn(EA[i], hs[i], EB[i]);
         }
-        if (on && t0 < a.S) {
+        if (on && t0 < S) {
             // segments are kSteps long and tiles a multiple of 64: a chunk starts where a segment does
             if (ck && (t0 & (kChunk - 1)) == 0 && t0 < L) store<float, V>(ck + (size_t)(t0 / kChunk) * a.D, hs);
             char *o = out + (size_t)t0 * row_x;
@@ -210,15 +204,15 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
 #pragma unroll
                 for (int j = 0; j < kSteps; ++j) {
 #pragma unroll
-                    for (int i = 0; i < P; ++i) hs[i] = fma2(av[j][i], hs[i], bv[j][i]);
+                    for (int i = 0; i < P; ++i) hs[i] = __ffma2_rn(av[j][i], hs[i], bv[j][i]);
                     store<T, V>(o + j * (size_t)row_x, hs);
                 }
             } else {
-                const int n = (int)min((long long)kSteps, a.S - t0), nv = (int)max(0LL, L - t0);
+                const int n = (int)min((unsigned)kSteps, S - t0), nv = t0 < L ? (int)(L - t0) : 0;
 #pragma unroll
                 for (int j = 0; j < kSteps; ++j) {
 #pragma unroll
-                    for (int i = 0; i < P; ++i) hs[i] = j < nv ? fma2(av[j][i], hs[i], bv[j][i]) : 0;
+                    for (int i = 0; i < P; ++i) hs[i] = j < nv ? __ffma2_rn(av[j][i], hs[i], bv[j][i]) : both(0.f);
                     if (j < n) store<T, V>(o + j * (size_t)row_x, hs);
                 }
             }
@@ -227,9 +221,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
     if (R > 1) cluster_meet();  // a block that gave up must not leave while the others write to it
     if (!on) return;
     // tokens behind the last tile
-    f2_t zero[P];
+    float2 zero[P];
     fill(zero, 0.f);
-    for (long long t = tiles * step + (long long)rank * (kThreads / lx) + seg; t < a.S; t += (long long)R * (kThreads / lx))
+    for (unsigned t = tiles * step + rank * (kThreads / lx) + seg; t < S; t += R * (kThreads / lx))
         store<T, V>(out + (size_t)t * row_x, zero);
     if (a.final_state && Lr >= 0 && seg == 0 && rank == 0) store<float, V>(a.final_state + (size_t)bn * a.D + c0, h);
 }
@@ -248,7 +242,7 @@ template <typename T, typename G, bool kMix> cudaError_t launch_m(const ScanArgs
     const long long rows = (long long)a.B * a.N;
     const int blocks = 2 * sm_count();
     if (a.D % 4 == 0) {
-        const Cut cut = choose_cut(rows, a.D, 4, a.S, kSteps, 32, 4, blocks);
+        const Cut cut = choose_cut(rows, a.D, 4, a.S, kSteps, wide_rows<T>(a.D) ? 32 : 16, 4, blocks);
         return cut.lx == 32 ? launch_v<T, G, kMix, 4, true>(a, cut, s) : launch_v<T, G, kMix, 4, false>(a, cut, s);
     }
     if (a.D % 2 == 0) return launch_v<T, G, kMix, 2, false>(a, choose_cut(rows, a.D, 2, a.S, kSteps, 16, 4, blocks), s);

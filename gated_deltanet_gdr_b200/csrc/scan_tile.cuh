@@ -11,8 +11,8 @@
 // their tiles' (A, B) through distributed shared memory.
 #pragma once
 
-#include "common.cuh"
 #include "kernels.h"
+#include "pairs.cuh"
 #include "sm100.cuh"
 
 namespace gdr {
@@ -21,22 +21,6 @@ namespace scan {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxRanks = 8;  // blocks of a cluster (the portable limit)
-
-// ---- channels in pairs (f32x2 arithmetic) ------------------------------------------------------------------------
-
-template <int V> constexpr int kPairs = (V + 1) / 2;  // a single channel fills half of one
-
-__device__ __forceinline__ f2_t add2(f2_t a, f2_t b) {
-    f2_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ f2_t both(float x) { return pk2(x, x); }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // a = e^g, and (kRest) rest = 1 - e^g, of a pair.  Near 0 the Taylor series, whose first dropped term is below a tenth
 // of a rounding (2^-24) of a for |g| < 1/8, or below one rounding of the rest for |g| < 1/4: the rest keeps its digits, and
@@ -63,13 +47,13 @@ template <bool kRest> __device__ __forceinline__ void decay(float g, float &a, f
         a = fabsf(g) < 0.125f ? p : far;
     }
 }
-template <bool kRest> __device__ __forceinline__ void decay(f2_t g, f2_t &a, f2_t &rest) {
+template <bool kRest> __device__ __forceinline__ void decay(float2 g, float2 &a, float2 &rest) {
     float g0, g1, a0, a1, r0 = 0.f, r1 = 0.f;
     up2(g, g0, g1);
     decay<kRest>(g0, a0, r0);
     decay<kRest>(g1, a1, r1);
-    a = pk2(a0, a1);
-    rest = pk2(r0, r1);
+    a = make_float2(a0, a1);
+    rest = make_float2(r0, r1);
 }
 
 // length of sequence b, or -1 for one outside [0, S]
@@ -78,105 +62,6 @@ __device__ __forceinline__ int seq_len(const int32_t *lengths, int b, int S) {
     return (L < 0 || L > S) ? -1 : L;
 }
 
-// ---- V consecutive elements ------------------------------------------------------------------------------------
-
-template <int N> struct Raw;
-template <> struct Raw<2> { using type = unsigned short; };
-template <> struct Raw<4> { using type = unsigned; };
-template <> struct Raw<8> { using type = uint2; };
-template <> struct Raw<16> { using type = uint4; };
-template <typename T, int V> using RawV = typename Raw<(int)sizeof(T) * V>::type;
-
-
-template <typename T, int V> __device__ __forceinline__ void unpack(const RawV<T, V> &r, f2_t (&x)[kPairs<V>]) {
-    const T *e = reinterpret_cast<const T *>(&r);
-#pragma unroll
-    for (int i = 0; i < kPairs<V>; ++i) x[i] = pk2(to_f32(e[2 * i]), 2 * i + 1 < V ? to_f32(e[2 * i + 1 < V ? 2 * i + 1 : 0]) : 0.f);
-}
-template <typename T, int V> __device__ __forceinline__ void store(void *p, const f2_t (&x)[kPairs<V>]) {
-    RawV<T, V> r;
-    T *e = reinterpret_cast<T *>(&r);
-#pragma unroll
-    for (int i = 0; i < kPairs<V>; ++i) {
-        float lo, hi;
-        up2(x[i], lo, hi);
-        e[2 * i] = from_f32<T>(lo);
-        if (2 * i + 1 < V) e[2 * i + 1 < V ? 2 * i + 1 : 0] = from_f32<T>(hi);
-    }
-    *static_cast<RawV<T, V> *>(p) = r;
-}
-template <int V> __device__ __forceinline__ void load_f32(const float *p, f2_t (&x)[kPairs<V>]) {
-    unpack<float, V>(*reinterpret_cast<const RawV<float, V> *>(p), x);
-}
-template <int P> __device__ __forceinline__ void fill(f2_t (&x)[P], float v) {
-#pragma unroll
-    for (int i = 0; i < P; ++i) x[i] = both(v);
-}
-// pair x from the lane `d` below (or above: the shuffles of a pair are two)
-__device__ __forceinline__ f2_t shfl_up2(f2_t x, int d) {
-    float lo, hi;
-    up2(x, lo, hi);
-    return pk2(__shfl_up_sync(0xffffffffu, lo, d), __shfl_up_sync(0xffffffffu, hi, d));
-}
-__device__ __forceinline__ f2_t shfl_down2(f2_t x, int d) {
-    float lo, hi;
-    up2(x, lo, hi);
-    return pk2(__shfl_down_sync(0xffffffffu, lo, d), __shfl_down_sync(0xffffffffu, hi, d));
-}
-
-// ---- staging: every thread copies its own inputs to a place of its own, so that no barrier is needed to read them --
-
-// copies one element vector to shared memory, or zeros where !on (src is then not read)
-template <typename R, bool kMask> __device__ __forceinline__ void stage(R *dst, const void *src, bool on) {
-    if constexpr (sizeof(R) >= 4) {
-        const unsigned d = (unsigned)__cvta_generic_to_shared(dst);
-        if constexpr (!kMask) {
-            if constexpr (sizeof(R) == 16)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
-            else
-                asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(sizeof(R)) : "memory");
-        } else {
-            const int n = on ? (int)sizeof(R) : 0;
-            if constexpr (sizeof(R) == 16)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
-            else
-                asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(sizeof(R)), "r"(n)
-                             : "memory");
-        }
-    } else {
-        *dst = !kMask || on ? *static_cast<const R *>(src) : R{};
-    }
-}
-// a thread's TS tokens of one tensor, rows `row` bytes apart, n of them valid (the others zero); src is the first
-template <int TS, typename R>
-__device__ __forceinline__ void stage_segment(R (*dst)[kThreads], const void *src, unsigned row, int n) {
-    const char *p = static_cast<const char *>(src);
-    if (n == TS) {
-#pragma unroll
-        for (int j = 0; j < TS; ++j) stage<R, false>(&dst[j][threadIdx.x], p + j * (size_t)row, true);
-    } else {
-#pragma unroll
-        for (int j = 0; j < TS; ++j) stage<R, true>(&dst[j][threadIdx.x], j < n ? p + j * (size_t)row : p, j < n);
-    }
-}
-// the same for a warp whose lanes lie side by side over 32 * 8 bytes of a row: 16 bytes a lane, two rows an instruction.  p is
-// the row's start at the warp's first channel, `bytes` what the row still holds there (a multiple of 16, may be <= 0).
-// Lanes read what others copied: __syncwarp() after the wait and before the next copy.
-template <int TS> __device__ __forceinline__ void stage_rows(uint2 (*dst)[kThreads], const char *p, unsigned row, int n, long long bytes) {
-    const int lane = threadIdx.x & 31, sub = lane >> 4, at = (lane & 15) * 16;
-    const bool on = at < bytes;
-#pragma unroll
-    for (int j = 0; j < TS; j += 2) {
-        const bool in = on && j + sub < n;
-        const unsigned d = (unsigned)__cvta_generic_to_shared(&dst[j + sub][threadIdx.x & ~31]) + at;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d),
-                     "l"(in ? p + (j + sub) * (size_t)row + at : p), "r"(in ? 16 : 0)
-                     : "memory");
-    }
-}
-__device__ __forceinline__ void stage_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void stage_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
-
 // ---- clusters -----------------------------------------------------------------------------------------------------
 
 // every thread of every block of the cluster passes together; orders no memory but mbarrier initialisations fenced before
@@ -184,7 +69,7 @@ __device__ __forceinline__ void cluster_meet() {
     asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 // writes V floats at `p` and their bytes to the count of `bar` (both given as this block's addresses) in block `rank`
-template <int V> __device__ __forceinline__ void put_remote(const float *p, const uint64_t *bar, int rank, const f2_t (&v)[kPairs<V>]) {
+template <int V> __device__ __forceinline__ void put_remote(const float *p, const uint64_t *bar, int rank, const float2 (&v)[kPairs<V>]) {
     float x[2 * kPairs<V>];
 #pragma unroll
     for (int i = 0; i < kPairs<V>; ++i) up2(v[i], x[2 * i], x[2 * i + 1]);
@@ -232,6 +117,9 @@ __device__ __forceinline__ bool wait_remote(uint64_t *bar, unsigned parity, uint
 }
 
 // ---- the cut -------------------------------------------------------------------------------------------------------
+
+// whether 32 lanes may lie over the channels: rows of 16-bit elements are then staged 16 bytes at a time
+template <typename T> bool wide_rows(int D) { return sizeof(T) == 4 || D % 8 == 0; }
 
 struct Cut {
     int lx;     // lanes side by side over the channels, a power of two

@@ -343,7 +343,7 @@ int gdr_conv1d(const void *x, const void *weight, const void *bias, const void *
  *   workspace, ws_bytes  device scratch of at least gdr_conv1d_bwd_workspace() bytes (the partial sums of dweight and
  *                        dbias), owned by the caller, 16-byte aligned; two calls in flight at once need separate ones
  * Everything but dweight and dbias is in dtype.  No output may overlap an input.  Constraints, and the length check,
- * as for gdr_conv1d; a sequence whose length is outside [0, S] contributes nothing (its dx and dconv_state_in rows
+ * as for gdr_conv1d, and C <= 2^26; a sequence whose length is outside [0, S] contributes nothing (its dx and dconv_state_in rows
  * are zero).  A shorter workspace returns GDR_ERR_WORKSPACE.
  */
 int gdr_conv1d_bwd(const void *x, const void *weight, const void *bias, const void *conv_state_in,
