@@ -444,62 +444,77 @@ def prepare_conv1d(x, weight, bias=None, conv_state=None, actual_seq_lengths=Non
 
 # ---- the conv1d's gradient, the gated linear recurrence and the state slots -------------------------------------
 #
-# These calls marshal for short kernels (a decode step, a handful of slots), so each looks at the current device and
-# stream once and passes plain integers to the C entry.  With ``stream=`` another than the current stream, the tensors
-# a call allocates belong to that stream, and the allocator is told which streams use what (``_uses``).
+# These calls marshal for short kernels (a decode step, a handful of slots), where a microsecond of checks is a
+# measurable share: each looks at the current device and stream once, checks a tensor in one expression (``_dev`` names
+# what is wrong with it only when something is), and passes plain integers to the C entry.  With ``stream=`` another than
+# the current stream, the tensors a call allocates belong to that stream, and the allocator is told which streams use what.
+
+_CODES = {torch.float32: GDR_F32, torch.bfloat16: GDR_BF16, torch.float16: GDR_F16}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
 
 class _Call:
-    """The device and stream of one call, and the tensors it touches."""
+    """The device and stream of one call, and the tensors it touches on another stream than the current one."""
     __slots__ = ("dev", "stream", "other", "used")
 
     def __init__(self, stream):
         self.dev = torch.cuda.current_device()
-        current = torch.cuda.current_stream()
+        self.stream = _raw_stream(self.dev)
         self.other = None
-        if stream is not None and stream.cuda_stream != current.cuda_stream:
+        if stream is not None and stream.cuda_stream != self.stream:
             if stream.device.index != self.dev:
                 raise RuntimeError(f"the stream is on {stream.device}, but the call runs on the current device "
                                    f"cuda:{self.dev}")
-            self.other, current = stream, stream
-        self.stream = current.cuda_stream
-        self.used = []
+            self.other, self.stream, self.used = stream, stream.cuda_stream, []
 
     def ptr(self, t, name, dtype, shape):
         """Address of a dense tensor of that type and shape on the current device; None for None."""
         if t is None:
             return None
-        if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or not t.is_cuda \
-                or t.device.index != self.dev or not t.is_contiguous():
-            _dev(t, name, dtype, shape)  # says which of them
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == self.dev
+                and t.is_contiguous()):
+            _dev(t, name, dtype, shape)
         if self.other is not None:
             self.used.append(t)
         return t.data_ptr()
 
-    def new(self, shape, dtype):
+    def out(self, t, name, ref, dtype=None, shape=None):
+        """The output t (checked) or, for None, a new one: as the dense tensor ref, or of a type and shape of its own
+        on ref's device.  Returns the tensor and its address."""
+        if t is not None:
+            return t, self.ptr(t, name, dtype or ref.dtype, ref.shape if shape is None else shape)
         if self.other is None:
-            return torch.empty(shape, dtype=dtype, device=self.dev)
-        with torch.cuda.stream(self.other):
-            t = torch.empty(shape, dtype=dtype, device=self.dev)
-        t.record_stream(torch.cuda.current_stream())
-        return t
+            t = torch.empty_like(ref) if shape is None else ref.new_empty(shape, dtype=dtype)
+        else:
+            with torch.cuda.stream(self.other):
+                t = torch.empty_like(ref) if shape is None else ref.new_empty(shape, dtype=dtype)
+            t.record_stream(torch.cuda.current_stream())
+        return t, t.data_ptr()
 
     def done(self, status, what):
-        for t in self.used:
-            t.record_stream(self.other)
+        if self.other is not None:
+            for t in self.used:
+                t.record_stream(self.other)
         if status != GDR_OK:
             _check(status, what)
 
 
-def _four(x, name):
+def _sizes(x, name):
     if not isinstance(x, torch.Tensor) or x.dim() != 4:
         raise ValueError(f"{name} must be a (B, N, S, D) tensor")
     return x.shape
 
 
+def _code(dt):
+    c = _CODES.get(dt)
+    return _dtype_code(dt) if c is None else c
+
+
 def _gate_code(x, g):
-    if not isinstance(g, torch.Tensor) or (g.dtype != torch.float32 and g.dtype != x.dtype):
+    if not isinstance(g, torch.Tensor) or (g.dtype is not torch.float32 and g.dtype is not x.dtype):
         raise RuntimeError("g must be a float32 tensor or have the dtype of x")
-    return _dtype_code(g.dtype)
+    return _code(g.dtype)
 
 
 def scan_checkpoint_shape(B: int, N: int, S: int, D: int):
@@ -509,22 +524,20 @@ def scan_checkpoint_shape(B: int, N: int, S: int, D: int):
 
 def _scan_fwd_args(x, g, initial_state, actual_seq_lengths, mix, out, final_state, output_final_state, checkpoints,
                    output_checkpoints, stream):
-    B, N, S, D = _four(x, "x")
-    dt, code = x.dtype, _dtype_code(x.dtype)
+    B, N, S, D = _sizes(x, "x")
+    dt, code = x.dtype, _code(x.dtype)
     gcode = _gate_code(x, g)
     c = _Call(stream)
     px, pg = c.ptr(x, "x", dt, x.shape), c.ptr(g, "g", g.dtype, x.shape)
     pi = c.ptr(initial_state, "initial_state", torch.float32, (B, N, D))
     pl = c.ptr(actual_seq_lengths, "actual_seq_lengths", torch.int32, (B,))
-    if out is None:
-        out = c.new((B, N, S, D), dt)
-    if final_state is None and output_final_state:
-        final_state = c.new((B, N, D), torch.float32)
-    if checkpoints is None and output_checkpoints:
-        checkpoints = c.new(scan_checkpoint_shape(B, N, S, D), torch.float32)
-    args = (px, pg, pi, pl, B, N, S, D, code, gcode, int(bool(mix)), c.ptr(out, "out", dt, (B, N, S, D)),
-            c.ptr(final_state, "final_state", torch.float32, (B, N, D)),
-            c.ptr(checkpoints, "checkpoints", torch.float32, scan_checkpoint_shape(B, N, S, D)), c.stream)
+    out, po = c.out(out, "out", x)
+    pf = pc = None
+    if final_state is not None or output_final_state:
+        final_state, pf = c.out(final_state, "final_state", x, torch.float32, (B, N, D))
+    if checkpoints is not None or output_checkpoints:
+        checkpoints, pc = c.out(checkpoints, "checkpoints", x, torch.float32, scan_checkpoint_shape(B, N, S, D))
+    args = (px, pg, pi, pl, B, N, S, D, code, gcode, 1 if mix else 0, po, pf, pc, c.stream)
     return c, args, (out, final_state, checkpoints)
 
 
@@ -538,7 +551,7 @@ def scan_fwd(x, g, initial_state=None, actual_seq_lengths=None, *, mix: bool = F
     states that ``scan_bwd`` needs.  ``final_state`` may be ``initial_state`` (in-place update)."""
     c, args, res = _scan_fwd_args(x, g, initial_state, actual_seq_lengths, mix, out, final_state, output_final_state,
                                   checkpoints, output_checkpoints, stream)
-    c.done(lib().gdr_scan_fwd(*args), "gdr_scan_fwd")
+    c.done((_lib or lib()).gdr_scan_fwd(*args), "gdr_scan_fwd")
     return res
 
 
@@ -549,15 +562,15 @@ def prepare_scan_fwd(x, g, initial_state=None, actual_seq_lengths=None, *, mix: 
     c, args, res = _scan_fwd_args(x, g, initial_state, actual_seq_lengths, mix, out, final_state, output_final_state,
                                   checkpoints, output_checkpoints, stream)
     c.done(GDR_OK, "gdr_scan_fwd")
-    return PreparedCall(lib().gdr_scan_fwd, args, "gdr_scan_fwd", res)
+    return PreparedCall((_lib or lib()).gdr_scan_fwd, args, "gdr_scan_fwd", res)
 
 
 def scan_bwd(x, g, checkpoints, dout, dfinal_state=None, actual_seq_lengths=None, *, mix: bool = False, dx=None,
              dg=None, dinitial_state=None, output_dinitial_state: bool = True, stream=None):
     """Gradient of ``scan_fwd`` (``gdr_scan_bwd``) from the checkpoints it kept, for the gradients dout (B, N, S, D) of
     out and dfinal_state (B, N, D) of final_state.  Returns (dx, dg, dinitial_state or None)."""
-    B, N, S, D = _four(x, "x")
-    dt, code = x.dtype, _dtype_code(x.dtype)
+    B, N, S, D = _sizes(x, "x")
+    dt, code = x.dtype, _code(x.dtype)
     gcode = _gate_code(x, g)
     c = _Call(stream)
     px, pg = c.ptr(x, "x", dt, x.shape), c.ptr(g, "g", g.dtype, x.shape)
@@ -565,23 +578,21 @@ def scan_bwd(x, g, checkpoints, dout, dfinal_state=None, actual_seq_lengths=None
     pd = c.ptr(dout, "dout", dt, x.shape)
     pf = c.ptr(dfinal_state, "dfinal_state", torch.float32, (B, N, D))
     pl = c.ptr(actual_seq_lengths, "actual_seq_lengths", torch.int32, (B,))
-    if dx is None:
-        dx = c.new((B, N, S, D), dt)
-    if dg is None:
-        dg = c.new((B, N, S, D), g.dtype)
-    if dinitial_state is None and output_dinitial_state:
-        dinitial_state = c.new((B, N, D), torch.float32)
-    st = lib().gdr_scan_bwd(px, pg, pc, pd, pf, pl, B, N, S, D, code, gcode, int(bool(mix)),
-                            c.ptr(dx, "dx", dt, x.shape), c.ptr(dg, "dg", g.dtype, x.shape),
-                            c.ptr(dinitial_state, "dinitial_state", torch.float32, (B, N, D)), c.stream)
+    dx, px_ = c.out(dx, "dx", x)
+    dg, pg_ = c.out(dg, "dg", g)
+    pi_ = None
+    if dinitial_state is not None or output_dinitial_state:
+        dinitial_state, pi_ = c.out(dinitial_state, "dinitial_state", x, torch.float32, (B, N, D))
+    st = (_lib or lib()).gdr_scan_bwd(px, pg, pc, pd, pf, pl, B, N, S, D, code, gcode, 1 if mix else 0, px_, pg_, pi_,
+                                      c.stream)
     c.done(st, "gdr_scan_bwd")
     return dx, dg, dinitial_state
 
 
 def _scan_step_args(x, g, state_pool, ssm_state_indices, actual_seq_lengths, num_accepted_tokens, mix, out, per_token,
                     stream):
-    B, N, S, D = _four(x, "x")
-    dt, code = x.dtype, _dtype_code(x.dtype)
+    B, N, S, D = _sizes(x, "x")
+    dt, code = x.dtype, _code(x.dtype)
     gcode = _gate_code(x, g)
     if not isinstance(state_pool, torch.Tensor) or state_pool.dim() != 3:
         raise ValueError("state_pool must be a (slots, N, D) tensor")
@@ -594,10 +605,9 @@ def _scan_step_args(x, g, state_pool, ssm_state_indices, actual_seq_lengths, num
     ps = c.ptr(ssm_state_indices, "ssm_state_indices", torch.int32, ssm_state_indices.shape)
     pl = c.ptr(actual_seq_lengths, "actual_seq_lengths", torch.int32, (B,))
     pa = c.ptr(num_accepted_tokens, "num_accepted_tokens", torch.int32, (B,))
-    if out is None:
-        out = c.new((B, N, S, D), dt)
-    args = (px, pg, pp, slots, ps, pl, pa, B, N, S, D, code, gcode, int(bool(mix)), int(bool(per_token)),
-            c.ptr(out, "out", dt, x.shape), c.stream)
+    out, po = c.out(out, "out", x)
+    args = (px, pg, pp, slots, ps, pl, pa, B, N, S, D, code, gcode, 1 if mix else 0, 1 if per_token else 0, po,
+            c.stream)
     return c, args, (out, state_pool)
 
 
@@ -607,7 +617,7 @@ def scan_step(x, g, state_pool, ssm_state_indices, actual_seq_lengths=None, num_
     x, g (B, N, S, D) with S <= 8, index and length arrays as in ``recurrent_step``.  Returns (out, state_pool)."""
     c, args, res = _scan_step_args(x, g, state_pool, ssm_state_indices, actual_seq_lengths, num_accepted_tokens, mix,
                                    out, per_token, stream)
-    c.done(lib().gdr_scan_step(*args), "gdr_scan_step")
+    c.done((_lib or lib()).gdr_scan_step(*args), "gdr_scan_step")
     return res
 
 
@@ -617,12 +627,12 @@ def prepare_scan_step(x, g, state_pool, ssm_state_indices, actual_seq_lengths=No
     c, args, res = _scan_step_args(x, g, state_pool, ssm_state_indices, actual_seq_lengths, num_accepted_tokens, mix,
                                    out, per_token, stream)
     c.done(GDR_OK, "gdr_scan_step")
-    return PreparedCall(lib().gdr_scan_step, args, "gdr_scan_step", res)
+    return PreparedCall((_lib or lib()).gdr_scan_step, args, "gdr_scan_step", res)
 
 
 def conv1d_bwd_workspace_bytes(B: int, S: int, Nk: int, Nv: int, Dk: int, Dv: int, K: int) -> int:
     """Bytes of workspace ``gdr_conv1d_bwd`` needs for these sizes."""
-    return int(lib().gdr_conv1d_bwd_workspace(B, S, Nk, Nv, Dk, Dv, K))
+    return int((_lib or lib()).gdr_conv1d_bwd_workspace(B, S, Nk, Nv, Dk, Dv, K))
 
 
 def conv1d_bwd(x, weight, dq, dk, dv, bias=None, conv_state=None, actual_seq_lengths=None, dconv_state_out=None, *,
@@ -634,36 +644,29 @@ def conv1d_bwd(x, weight, dq, dk, dv, bias=None, conv_state=None, actual_seq_len
         raise ValueError("x must be (B, S, C) and weight (C, K)")
     B, S, C = x.shape
     K = weight.shape[1]
-    _, Nk, _, Dk = _four(dq, "dq")
-    _, Nv, _, Dv = _four(dv, "dv")
+    _, Nk, _, Dk = _sizes(dq, "dq")
+    _, Nv, _, Dv = _sizes(dv, "dv")
     if C != 2 * Nk * Dk + Nv * Dv:
         raise ValueError(f"x has {C} channels; 2 * Nk * Dk + Nv * Dv = {2 * Nk * Dk + Nv * Dv}")
-    dt, code = x.dtype, _dtype_code(x.dtype)
+    dt, code = x.dtype, _code(x.dtype)
     c = _Call(stream)
     ins = (c.ptr(x, "x", dt, x.shape), c.ptr(weight, "weight", dt, (C, K)), c.ptr(bias, "bias", dt, (C,)),
            c.ptr(conv_state, "conv_state", dt, (B, C, K)),
            c.ptr(actual_seq_lengths, "actual_seq_lengths", torch.int32, (B,)), c.ptr(dq, "dq", dt, (B, Nk, S, Dk)),
            c.ptr(dk, "dk", dt, (B, Nk, S, Dk)), c.ptr(dv, "dv", dt, (B, Nv, S, Dv)),
            c.ptr(dconv_state_out, "dconv_state_out", dt, (B, C, K)))
-    need = conv1d_bwd_workspace_bytes(B, S, Nk, Nv, Dk, Dv, K)
-    if workspace is None:
-        workspace = c.new((need,), torch.uint8) if need else None
-    elif workspace.numel() < need:
+    need = (_lib or lib()).gdr_conv1d_bwd_workspace(B, S, Nk, Nv, Dk, Dv, K)
+    if workspace is not None and workspace.numel() < need:
         raise ValueError(f"workspace holds {workspace.numel()} bytes; the call needs {need}")
-    if dx is None:
-        dx = c.new((B, S, C), dt)
-    if dweight is None:
-        dweight = c.new((C, K), torch.float32)
-    if dbias is None:
-        dbias = c.new((C,), torch.float32)
-    if dconv_state is None:
-        dconv_state = c.new((B, C, K), dt)
-    st = lib().gdr_conv1d_bwd(*ins, B, S, Nk, Nv, Dk, Dv, K, code, c.ptr(dx, "dx", dt, (B, S, C)),
-                              c.ptr(dweight, "dweight", torch.float32, (C, K)),
-                              c.ptr(dbias, "dbias", torch.float32, (C,)),
-                              c.ptr(dconv_state, "dconv_state", dt, (B, C, K)),
-                              c.ptr(workspace, "workspace", torch.uint8, None if workspace is None else workspace.shape),
-                              0 if workspace is None else workspace.numel(), c.stream)
+    pw = None
+    if workspace is not None or need:
+        workspace, pw = c.out(workspace, "workspace", x, torch.uint8, (need,) if workspace is None else workspace.shape)
+    dx, px = c.out(dx, "dx", x)
+    dweight, pdw = c.out(dweight, "dweight", x, torch.float32, (C, K))
+    dbias, pdb = c.out(dbias, "dbias", x, torch.float32, (C,))
+    dconv_state, pds = c.out(dconv_state, "dconv_state", x, dt, (B, C, K))
+    st = (_lib or lib()).gdr_conv1d_bwd(*ins, B, S, Nk, Nv, Dk, Dv, K, code, px, pdw, pdb, pds, pw,
+                                        0 if workspace is None else workspace.numel(), c.stream)
     c.done(st, "gdr_conv1d_bwd")
     return dx, dweight, dbias, dconv_state
 
@@ -700,7 +703,7 @@ def slot_copy(pools, src, dst, *, stream=None):
     c = _Call(stream)
     arr, n_pools, slots = _pools(c, pools)
     ps = _list_i32(c, src, "src")
-    st = lib().gdr_slot_copy(arr, n_pools, slots, ps, _list_i32(c, dst, "dst", src.shape[0]), src.shape[0], c.stream)
+    st = (_lib or lib()).gdr_slot_copy(arr, n_pools, slots, ps, _list_i32(c, dst, "dst", src.shape[0]), src.shape[0], c.stream)
     c.done(st, "gdr_slot_copy")
     return pools
 
@@ -714,9 +717,8 @@ def slot_fork(pools, slot_table, parents, *, new_slot_table=None, stream=None):
     pt = _list_i32(c, slot_table, "slot_table")
     n = slot_table.shape[0]
     pp = _list_i32(c, parents, "parents", n)
-    if new_slot_table is None:
-        new_slot_table = c.new((n,), torch.int32)
-    st = lib().gdr_slot_fork(arr, n_pools, slots, pt, pp, n, _list_i32(c, new_slot_table, "new_slot_table", n), c.stream)
+    new_slot_table, pn = c.out(new_slot_table, "new_slot_table", slot_table)
+    st = (_lib or lib()).gdr_slot_fork(arr, n_pools, slots, pt, pp, n, pn, c.stream)
     c.done(st, "gdr_slot_fork")
     return new_slot_table
 
@@ -728,12 +730,9 @@ def slot_compact(pools, live, *, new_slot=None, n_live=None, stream=None):
     c = _Call(stream)
     arr, n_pools, slots = _pools(c, pools)
     pl = _list_i32(c, live, "live", slots)
-    if new_slot is None:
-        new_slot = c.new((slots,), torch.int32)
-    if n_live is None:
-        n_live = c.new((1,), torch.int32)
-    st = lib().gdr_slot_compact(arr, n_pools, slots, pl, _list_i32(c, new_slot, "new_slot", slots),
-                                _list_i32(c, n_live, "n_live", 1), c.stream)
+    new_slot, pn = c.out(new_slot, "new_slot", live)
+    n_live, pc = c.out(n_live, "n_live", live, torch.int32, (1,))
+    st = (_lib or lib()).gdr_slot_compact(arr, n_pools, slots, pl, pn, pc, c.stream)
     c.done(st, "gdr_slot_compact")
     return new_slot, n_live
 
@@ -745,7 +744,7 @@ def slot_free(pools, idx, live=None, *, stream=None):
     arr, n_pools, slots = _pools(c, pools)
     pi = _list_i32(c, idx, "idx")
     pl = None if live is None else _list_i32(c, live, "live", slots)
-    st = lib().gdr_slot_free(arr, n_pools, slots, pi, idx.shape[0], pl, c.stream)
+    st = (_lib or lib()).gdr_slot_free(arr, n_pools, slots, pi, idx.shape[0], pl, c.stream)
     c.done(st, "gdr_slot_free")
     return pools
 

@@ -3,7 +3,7 @@
 // pre[u] = bias + sum_j w_j x[u - K + 1 + j];  dpre[u] = dy[u] silu'(pre[u]);
 // dx[t] = sum_j w_j dpre[t + K - 1 - j];  dw_j = sum_u dpre[u] x[u - K + 1 + j];  db = sum_u dpre[u].
 //
-// One thread owns 4 channels and walks kSub tokens and the K - 1 behind them (whose dpre reaches back into its tokens),
+// One thread owns 4 channels and walks up to 64 tokens and the K - 1 behind them (whose dpre reaches back into its tokens),
 // with a window of the last K inputs and of the last K dpre in registers.  The forward pass is computed again on the
 // way, so x and dy are read and dx written once, apart from the K - 1 tokens at either end, which the neighbouring warps
 // of the block read too.  Tokens come in batches of kBatch through a two-stage ring in shared memory (cp.async, every
@@ -18,8 +18,7 @@ namespace {
 
 constexpr int kWarps = 4;             // warps of a block, adjacent in time
 constexpr int kThreads = kWarps * 32;
-constexpr int kSub = 64;              // tokens a warp walks
-constexpr int kTile = kWarps * kSub;  // tokens of a block
+constexpr int kMaxSub = 64;           // most tokens that a warp walks, which bounds the terms of a thread's sums
 constexpr int kBatch = 8;             // tokens of a stage
 constexpr int V = 4;                  // channels of a thread
 constexpr int P = V / 2;
@@ -28,15 +27,12 @@ constexpr int P = V / 2;
 template <typename T>
 __device__ __forceinline__ const T *dy_base(const ConvBwdArgs &a, int b, int c0, int &row) {
     const int qk = a.Nk * a.Dk;
-    if (c0 < 2 * qk) {
-        const void *p = c0 < qk ? a.dq : a.dk;
-        const int c = c0 < qk ? c0 : c0 - qk;
-        row = a.Dk;
-        return static_cast<const T *>(p) + ((size_t)b * a.Nk + c / a.Dk) * a.S * a.Dk + c % a.Dk;
-    }
-    const int c = c0 - 2 * qk;
-    row = a.Dv;
-    return static_cast<const T *>(a.dv) + ((size_t)b * a.Nv + c / a.Dv) * a.S * a.Dv + c % a.Dv;
+    const bool v = c0 >= 2 * qk;
+    const void *p = v ? a.dv : c0 < qk ? a.dq : a.dk;
+    const int c = v ? c0 - 2 * qk : c0 < qk ? c0 : c0 - qk;
+    row = v ? a.Dv : a.Dk;
+    const int head = c >> (31 - __clz(row));  // head sizes are powers of two
+    return static_cast<const T *>(p) + ((size_t)b * (v ? a.Nv : a.Nk) + head) * a.S * row + (c & (row - 1));
 }
 
 __device__ __forceinline__ float rcp(float x) {
@@ -61,14 +57,14 @@ template <typename T> struct Stage {
 template <typename T, int K> constexpr int kBlocks = K <= 4 ? 4 : 3;
 
 template <typename T, int K>
-__global__ void __launch_bounds__(kThreads, (kBlocks<T, K>)) conv1d_bwd_kernel(const ConvBwdArgs a) {
+__global__ void __launch_bounds__(kThreads, (kBlocks<T, K>)) conv1d_bwd_kernel(const ConvBwdArgs a, const int sub) {
     extern __shared__ __align__(16) unsigned char smem[];
     auto &sm = *reinterpret_cast<Stage<T> *>(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int c0 = (blockIdx.x * 32 + lane) * V;
     const bool on = c0 < a.C;
     const int b = blockIdx.z;
-    const int t0 = blockIdx.y * kTile + warp * kSub, t1 = min(t0 + kSub, a.S);
+    const int t0 = (blockIdx.y * kWarps + warp) * sub, t1 = min(t0 + sub, a.S);
     const int Lr = a.lengths ? a.lengths[b] : a.S;
     const bool bad = Lr < 0 || Lr > a.S;
     if (bad && blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) raise_device_error(a.err, GDR_DEVERR_LENGTH);
@@ -255,7 +251,17 @@ __global__ void zero_f32_kernel(float *p, size_t n) {
     if (i < n) p[i] = 0.f;
 }
 
-int tiles(int S) { return (S + kTile - 1) / kTile; }
+// Tokens a warp walks: 64, or fewer (down to 16) where blocks of 64 would not even give every SM one -- the walk is the
+// call's latency then, and the K - 1 tokens read twice cost nothing (1 x 4096 tokens, 384 channels, bf16:
+// 16 us with 32 tokens, 20 with 64)
+int sub_for(int B, int S, int C) {
+    int sub = kMaxSub;
+    const long long groups = (long long)B * ((C + 32 * V - 1) / (32 * V));
+    while (sub > 16 && groups * ((S + (long long)kWarps * sub - 1) / (kWarps * sub)) < sm_count()) sub /= 2;
+    return sub;
+}
+// blocks along the tokens: at most 65535, since S <= 65535 * 64 and fewer tokens a warp come with fewer blocks
+int tiles(int S, int sub) { return (int)((S + (long long)kWarps * sub - 1) / (kWarps * sub)); }
 
 template <typename T, int K>
 cudaError_t launch_tk(const ConvBwdArgs &a, cudaStream_t s) {
@@ -264,8 +270,9 @@ cudaError_t launch_tk(const ConvBwdArgs &a, cudaStream_t s) {
     cudaError_t e = cache.allow_smem(smem);
     if (e != cudaSuccess) return e;
     const unsigned gx = (unsigned)((a.C + 32 * V - 1) / (32 * V));
-    const unsigned gy = (unsigned)(a.S > 0 ? tiles(a.S) : 1);  // without tokens, the state's gradient alone
-    conv1d_bwd_kernel<T, K><<<dim3(gx, gy, a.B), kThreads, smem, s>>>(a);
+    const int sub = sub_for(a.B, a.S, a.C);
+    const unsigned gy = (unsigned)(a.S > 0 ? tiles(a.S, sub) : 1);  // without tokens, the state's gradient alone
+    conv1d_bwd_kernel<T, K><<<dim3(gx, gy, a.B), kThreads, smem, s>>>(a, sub);
     e = cudaGetLastError();
     if (e != cudaSuccess || !a.partial) return e;
     conv1d_bwd_sum_kernel<<<dim3((unsigned)((a.C + 31) / 32), K + 1), 1024, 0, s>>>(a.partial, (int)(a.B * gy), a.C, K,
@@ -291,7 +298,7 @@ cudaError_t launch_t(const ConvBwdArgs &a, int K, cudaStream_t s) {
 }  // namespace
 
 size_t conv1d_bwd_workspace(int B, int S, int C, int K) {
-    return (size_t)B * tiles(S) * (K + 1) * C * sizeof(float);
+    return (size_t)B * tiles(S, sub_for(B, S, C)) * (K + 1) * C * sizeof(float);
 }
 
 cudaError_t launch_conv1d_bwd(const ConvBwdArgs &a, int K, gdr_dtype dt, cudaStream_t s) {
