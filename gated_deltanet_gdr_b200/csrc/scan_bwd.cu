@@ -324,15 +324,15 @@ template <typename T, typename G, bool kMix> cudaError_t launch_m(const ScanBwdA
     constexpr int kSteps = kStepsOf<T, kMix>, kMin = 32 * kSteps / kChunk;
     constexpr bool kCanBeWide = kSteps == 8;
     const long long rows = (long long)a.B * a.N;
-    const int blocks = kBlocksOf<T, kMix> * sm_count();
+    constexpr int kResident = kBlocksOf<T, kMix>;
     if (a.D % 4 == 0) {
-        const Cut cut = choose_cut(rows, a.D, 4, a.S, kSteps, kCanBeWide && wide_rows<T>(a.D) ? 32 : 16, kMin, blocks);
+        const Cut cut = choose_cut(rows, a.D, 4, a.S, kSteps, kCanBeWide && wide_rows<T>(a.D) ? 32 : 16, kMin, kResident);
         if constexpr (kCanBeWide)
             if (cut.lx == 32) return launch_v<T, G, kMix, 4, true>(a, cut, s);
         return launch_v<T, G, kMix, 4, false>(a, cut, s);
     }
-    if (a.D % 2 == 0) return launch_v<T, G, kMix, 2, false>(a, choose_cut(rows, a.D, 2, a.S, kSteps, 16, kMin, blocks), s);
-    return launch_v<T, G, kMix, 1, false>(a, choose_cut(rows, a.D, 1, a.S, kSteps, 16, kMin, blocks), s);
+    if (a.D % 2 == 0) return launch_v<T, G, kMix, 2, false>(a, choose_cut(rows, a.D, 2, a.S, kSteps, 16, kMin, kResident), s);
+    return launch_v<T, G, kMix, 1, false>(a, choose_cut(rows, a.D, 1, a.S, kSteps, 16, kMin, kResident), s);
 }
 template <typename T, typename G> cudaError_t launch_t(const ScanBwdArgs &a, cudaStream_t s) {
     return a.mode == GDR_SCAN_MIX ? launch_m<T, G, true>(a, s) : launch_m<T, G, false>(a, s);

@@ -240,13 +240,12 @@ cudaError_t launch_v(const ScanArgs &a, const Cut &cut, cudaStream_t s) {
 // vectors of 4 channels where rows are made of whole ones, of 2, else single channels
 template <typename T, typename G, bool kMix> cudaError_t launch_m(const ScanArgs &a, cudaStream_t s) {
     const long long rows = (long long)a.B * a.N;
-    const int blocks = 2 * sm_count();
     if (a.D % 4 == 0) {
-        const Cut cut = choose_cut(rows, a.D, 4, a.S, kSteps, wide_rows<T>(a.D) ? 32 : 16, 4, blocks);
+        const Cut cut = choose_cut(rows, a.D, 4, a.S, kSteps, wide_rows<T>(a.D) ? 32 : 16, 4, 2);
         return cut.lx == 32 ? launch_v<T, G, kMix, 4, true>(a, cut, s) : launch_v<T, G, kMix, 4, false>(a, cut, s);
     }
-    if (a.D % 2 == 0) return launch_v<T, G, kMix, 2, false>(a, choose_cut(rows, a.D, 2, a.S, kSteps, 16, 4, blocks), s);
-    return launch_v<T, G, kMix, 1, false>(a, choose_cut(rows, a.D, 1, a.S, kSteps, 16, 4, blocks), s);
+    if (a.D % 2 == 0) return launch_v<T, G, kMix, 2, false>(a, choose_cut(rows, a.D, 2, a.S, kSteps, 16, 4, 2), s);
+    return launch_v<T, G, kMix, 1, false>(a, choose_cut(rows, a.D, 1, a.S, kSteps, 16, 4, 2), s);
 }
 template <typename T, typename G> cudaError_t launch_t(const ScanArgs &a, cudaStream_t s) {
     return a.mode == GDR_SCAN_MIX ? launch_m<T, G, true>(a, s) : launch_m<T, G, false>(a, s);

@@ -20,7 +20,7 @@ namespace scan {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxRanks = 8;  // blocks of a cluster (the portable limit)
+constexpr int kMaxRanks = 8;  // most blocks of a cluster (the portable limit)
 
 // a = e^g, and (kRest) rest = 1 - e^g, of a pair.  Near 0 the Taylor series, whose first dropped term is below a tenth
 // of a rounding (2^-24) of a for |g| < 1/8, or below one rounding of the rest for |g| < 1/4: the rest keeps its digits, and
@@ -122,34 +122,45 @@ __device__ __forceinline__ bool wait_remote(uint64_t *bar, unsigned parity, uint
 template <typename T> bool wide_rows(int D) { return sizeof(T) == 4 || D % 8 == 0; }
 
 struct Cut {
-    int lx;     // lanes side by side over the channels, a power of two
+    int lx;     // lanes side by side over the channels, a power of two from 2 to 32
     int slabs;  // tiles over the channels
     int ranks;  // blocks of a cluster: consecutive tiles in time
 };
 
-// Lanes over the channels: the most that leave at most a quarter more lanes idle on this D than the best choice does.
-// Where the `want` blocks that the GPU holds are then not even half there, first clusters of up to 4 blocks, then fewer
-// lanes, then clusters of 8 (measured, forward, us: 128 rows of 128 channels and 4096 tokens 95 with 32 lanes and 2 blocks, 98
-// with 16 and 1; 4096 channels and 8192 tokens 67 with 16 lanes and 4 blocks, 70 with 32 and 8; 640 channels and 32769
-// tokens 78 with 8 lanes and 8 blocks, 89 with 16).  Less than 8 lanes come last: a row of so few channels is a sector or two.  No
-// cluster has a block that no token reaches.
-inline Cut choose_cut(long long rows, int D, int V, int S, int TS, int max_lx, int min_lx, long long want) {
-    Cut c{};
-    auto slabs_of = [&](int lx) { return (D + (long long)lx * V - 1) / ((long long)lx * V); };
-    long long least = -1;
-    for (int lx = max_lx; lx >= min_lx; lx /= 2)
-        if (least < 0 || slabs_of(lx) * lx < least) least = slabs_of(lx) * lx;
-    c.lx = max_lx;
-    while (slabs_of(c.lx) * c.lx * 4 > least * 5) c.lx /= 2;
-    auto tile = [&] { return (long long)TS * (kThreads / c.lx); };
-    auto room = [&] { return rows * slabs_of(c.lx) * c.ranks * 2 <= want && c.ranks * tile() < S; };
-    c.ranks = 1;
-    while (c.ranks < 4 && room()) c.ranks *= 2;
-    while (c.lx > 8 && room()) c.lx /= 2;
-    while (c.ranks < kMaxRanks && room()) c.ranks *= 2;
-    while (c.lx > min_lx && room()) c.lx /= 2;
-    c.slabs = (int)slabs_of(c.lx);
-    return c;
+// The cut of the least estimated time.  A block spends about the same time on every tile, whatever its shape (a little
+// more with fewer lanes, for the shuffles), so a cut costs the tiles that a block walks through, times what the blocks of
+// the fullest SM cost together: 1 for one, 0.8 more for each of the up to `resident` that share it at a time.  A cluster
+// lies within one of the GPU's groups of SMs, which are not multiples of it: kFit, as the occupancy query reports it.
+// Measured, forward, us: 640 channels and 32769 tokens, 8 lanes: 59 with clusters of 6 (20 of the 22 that fit), 67 of 5, 72 of 8
+// (15 fit), 77 of 7; 128 rows of 128 channels and 4096 tokens: 92 with 32 lanes and 2 blocks, 93 with 16 and 1, 102 with 8 and 1; 64
+// channels and 65536 tokens: 45 with 4 lanes and 8 blocks, 77 with 8 lanes.
+inline Cut choose_cut(long long rows, int D, int V, int S, int TS, int max_lx, int min_lx, int resident) {
+    // clusters of 1 .. 8 blocks that a B200 of 148 SMs holds with one block on an SM
+    constexpr int kFit[kMaxRanks] = {148, 74, 45, 33, 26, 22, 15, 15};
+    const int sms = sm_count();
+    auto together = [&](long long n) {
+        auto share = [](long long m) { return m ? 1.0 + 0.8 * (double)(m - 1) : 0.0; };
+        return (double)(n / resident) * share(resident) + share(n % resident);
+    };
+    Cut best{};
+    double least = 0;
+    for (int lx = max_lx; lx >= min_lx; lx /= 2) {
+        const long long slabs = (D + (long long)lx * V - 1) / ((long long)lx * V), clusters = rows * slabs;
+        const long long tile = (long long)TS * (kThreads / lx);
+        const double shuffles = lx == 32 ? 0.85 : lx == 16 ? 0.93 : lx == 8 ? 1.0 : lx == 4 ? 1.11 : 1.25;
+        for (int r = 1; r <= kMaxRanks && (r == 1 || (r - 1) * tile < S); ++r) {
+            const long long fit = kFit[r - 1] * sms >= 148 ? kFit[r - 1] * sms / 148 : 1;
+            const double t = shuffles * (1.0 + 0.02 * r) * (double)((S + r * tile - 1) / (r * tile)) *
+                             together((clusters + fit - 1) / fit);
+            if (!best.lx || t < least) {
+                least = t;
+                best.lx = lx;
+                best.slabs = (int)slabs;
+                best.ranks = r;
+            }
+        }
+    }
+    return best;
 }
 
 template <typename Args>
