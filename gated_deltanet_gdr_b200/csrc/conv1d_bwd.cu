@@ -128,8 +128,9 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, K>)) conv1d_bwd_kernel(c
 #pragma unroll
             for (int i = 0; i < V; ++i) ds_in[i * K] = from_f32<T>(ds_out && L == 0 ? to_f32(ds_out[i * K]) : 0.f);
 
-        // token u, at place j of the windows, its inputs at place p of stage s; whole: an ordinary one of the thread's tokens
-        auto step = [&](int u, int j, int s, int p, bool whole) {
+        // token u, at place j of the windows, its inputs at place p of stage s; whole: an ordinary one of the thread's
+        // tokens; halo: an ordinary one behind them
+        auto step = [&](int u, int j, int s, int p, bool whole, bool halo) {
             float2 g[P];
             unpack<T, V>(sm.x[s][p][tid], win[K - 1 + j]);
             unpack<T, V>(sm.dy[s][p][tid], g);
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, K>)) conv1d_bwd_kernel(c
                 for (int q = 0; q < K; ++q) pre = __ffma2_rn(w[q][i], win[j + q][i], pre);
                 const float2 d = __fmul2_rn(g[i], silu_slope(pre));
                 dwin[K - 1 + j][i] = d;
-                if (whole || u < t1) {
+                if (whole || (!halo && u < t1)) {
                     db[i] = __fadd2_rn(db[i], d);
 #pragma unroll
                     for (int q = 0; q < K; ++q) dw[q][i] = __ffma2_rn(d, win[j + q][i], dw[q][i]);
@@ -154,15 +155,15 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, K>)) conv1d_bwd_kernel(c
 #pragma unroll
                 for (int q = 1; q < K; ++q) r[i] = __ffma2_rn(w[q][i], dwin[j + K - 1 - q][i], r[i]);
             }
-            if (!whole && ds_out && t >= L - K && t < L) {
+            if (!whole && !halo && ds_out && t >= L - K && t < L) {
                 // the new state is the history from place L on: place q of it is position L - K + q
 #pragma unroll
                 for (int i = 0; i < P; ++i)
                     r[i] = __fadd2_rn(r[i], make_float2(to_f32(ds_out[2 * i * K + t - L + K]), to_f32(ds_out[(2 * i + 1) * K + t - L + K])));
             }
-            if ((whole && j >= K - 1) || t >= t0) {
+            if ((whole && j >= K - 1) || halo || t >= t0) {
                 store<T, V>(dx + (size_t)t * a.C, r);
-            } else if (!whole && ds_in) {
+            } else if (!whole && !halo && ds_in) {
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
                     float lo, hi;
@@ -189,12 +190,15 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, K>)) conv1d_bwd_kernel(c
             // takes part in the new state
             if ((u > t0 || !first) && u + kBatch <= t1 && (!ds_out || u + kBatch < L)) {
 #pragma unroll
-                for (int j = 0; j < kBatch; ++j) step(u + j, j, s, j, true);
+                for (int j = 0; j < kBatch; ++j) step(u + j, j, s, j, true, false);
                 shift(kBatch);
+            } else if (u == t1 && u >= t0 + kBatch && (!ds_out || u + K - 1 < L)) {  // the last K - 1
+#pragma unroll
+                for (int j = 0; j < K - 1; ++j) step(u + j, j, s, j, false, true);
             } else {
 #pragma unroll 1
                 for (int j = 0; j < kBatch && u + j < end; ++j) {
-                    step(u + j, 0, s, j, false);
+                    step(u + j, 0, s, j, false, false);
                     shift(1);
                 }
             }

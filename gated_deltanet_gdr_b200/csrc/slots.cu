@@ -1,9 +1,10 @@
 // slots.cu -- copying, forking, compacting and freeing slots of the state pools (gdr_slot_copy, gdr_slot_fork,
 // gdr_slot_compact, gdr_slot_free).
 //
-// All four are moves of whole slots (or zero fills), cut into pieces of kPiece bytes and dealt out evenly to the
-// resident blocks.  Which slots move is worked out on the device: every block derives the same plan from the index
-// arrays in its own shared memory, so one launch does everything and the host never waits for a count.
+// All four are moves of whole slots (or zero fills).  A slot is counted in units of kUnit bytes, and the units of all moves
+// are dealt out evenly, in runs, to the resident blocks.  Which slots move is worked out on the device: every block
+// derives the same plan from the index arrays in its own shared memory, so one launch does everything and the host never
+// waits for a count.  Bound by HBM.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -11,29 +12,29 @@ namespace gdr {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr unsigned kPiece = 32768;  // bytes of one work item: eight 16-byte accesses of every thread
+constexpr unsigned kUnit = kThreads * 16;  // bytes of a unit: one 16-byte access of every thread
+constexpr int kBatch = 8;                  // units whose loads are all issued before the first store
 
-// pieces of all pools of one slot, counted up: piece q belongs to the pool p with first[p] <= q < first[p + 1]
-struct Pieces {
+// units of all pools of one slot, counted up: unit q belongs to the pool p with first[p] <= q < first[p + 1]
+struct Units {
     unsigned first[GDR_MAX_POOLS + 1];
 };
 
-__device__ __forceinline__ void count_pieces(const SlotPools &p, Pieces &ps) {
+__device__ __forceinline__ void count_units(const SlotPools &p, Units &us) {
     if (threadIdx.x == 0) {
         unsigned at = 0;
         for (int i = 0; i < p.n; ++i) {
-            ps.first[i] = at;
-            at += (unsigned)((p.bytes[i] + kPiece - 1) / kPiece);
+            us.first[i] = at;
+            at += (unsigned)((p.bytes[i] + kUnit - 1) / kUnit);
         }
-        ps.first[p.n] = at;
+        us.first[p.n] = at;
     }
     __syncthreads();
 }
 
-// one piece in units of U; src NULL: zeros.  The loads of a batch are all issued before its first store.
+// up to kBatch units in elements of U; src NULL: zeros
 template <typename U>
-__device__ __forceinline__ void move_units(const char *src, char *dst, unsigned bytes) {
-    constexpr int kBatch = 8;
+__device__ __forceinline__ void move_elements(const char *src, char *dst, unsigned bytes) {
     const unsigned n = bytes / sizeof(U);
     const U *s = reinterpret_cast<const U *>(src);
     U *d = reinterpret_cast<U *>(dst);
@@ -50,23 +51,29 @@ __device__ __forceinline__ void move_units(const char *src, char *dst, unsigned 
     }
 }
 
-// moves piece q of slot src (negative: zeros) to slot dst
-__device__ __forceinline__ void move_piece(const SlotPools &p, const Pieces &ps, unsigned q, int src, int dst) {
+// moves units q .. of slot src (negative: zeros) to slot dst, at most `most` and kBatch of them, all of one pool; returns
+// how many
+__device__ __forceinline__ unsigned move_units(const SlotPools &p, const Units &us, unsigned q, unsigned long long most, int src,
+                                               int dst) {
     int i = 0;
-    while (q >= ps.first[i + 1]) ++i;
-    const unsigned long long sb = p.bytes[i], off = (unsigned long long)(q - ps.first[i]) * kPiece;
-    const unsigned n = (unsigned)(sb - off < kPiece ? sb - off : kPiece);
+    while (q >= us.first[i + 1]) ++i;
+    unsigned run = us.first[i + 1] - q;
+    if (run > (unsigned)kBatch) run = kBatch;
+    if (run > most) run = (unsigned)most;
+    const unsigned long long sb = p.bytes[i], off = (unsigned long long)(q - us.first[i]) * kUnit;
+    const unsigned n = (unsigned)(sb - off < run * kUnit ? sb - off : run * kUnit);
     const char *s = src < 0 ? nullptr : p.data[i] + (unsigned long long)src * sb + off;
     char *d = p.data[i] + (unsigned long long)dst * sb + off;
     // slots begin on the largest power of two up to 16 that divides their size
-    if ((sb & 15) == 0) move_units<uint4>(s, d, n);
-    else if ((sb & 7) == 0) move_units<uint2>(s, d, n);
-    else if ((sb & 3) == 0) move_units<unsigned>(s, d, n);
-    else if ((sb & 1) == 0) move_units<unsigned short>(s, d, n);
-    else move_units<unsigned char>(s, d, n);
+    if ((sb & 15) == 0) move_elements<uint4>(s, d, n);
+    else if ((sb & 7) == 0) move_elements<uint2>(s, d, n);
+    else if ((sb & 3) == 0) move_elements<unsigned>(s, d, n);
+    else if ((sb & 1) == 0) move_elements<unsigned short>(s, d, n);
+    else move_elements<unsigned char>(s, d, n);
+    return run;
 }
 
-// this block's share [lo, hi) of n items
+// this block's share [lo, hi) of n units
 __device__ __forceinline__ void share(unsigned long long n, unsigned long long &lo, unsigned long long &hi) {
     lo = n * blockIdx.x / gridDim.x;
     hi = n * (blockIdx.x + 1) / gridDim.x;
@@ -74,15 +81,16 @@ __device__ __forceinline__ void share(unsigned long long n, unsigned long long &
 
 __global__ void __launch_bounds__(kThreads) slot_copy_kernel(const SlotPools p, const int32_t *src, const int32_t *dst,
                                                              int n) {
-    __shared__ Pieces ps;
-    count_pieces(p, ps);
-    const unsigned per = ps.first[p.n];
+    __shared__ Units us;
+    count_units(p, us);
+    const unsigned per = us.first[p.n];
     unsigned long long lo, hi;
     share((unsigned long long)n * per, lo, hi);
     int now = -1, s = -1, d = -1;
     bool go = false;
-    for (unsigned long long it = lo; it < hi; ++it) {
+    for (unsigned long long it = lo; it < hi;) {
         const int i = (int)(it / per);
+        const unsigned q = (unsigned)(it - (unsigned long long)i * per);
         if (i != now) {  // the same for the whole block
             now = i;
             s = src[i];
@@ -105,26 +113,28 @@ __global__ void __launch_bounds__(kThreads) slot_copy_kernel(const SlotPools p, 
                 }
             }
         }
-        if (go) move_piece(p, ps, (unsigned)(it % per), s, d);
+        it += go ? move_units(p, us, q, hi - it, s, d) : per - q;
     }
 }
 
 __global__ void __launch_bounds__(kThreads) slot_free_kernel(const SlotPools p, const int32_t *idx, int n,
                                                              int32_t *live) {
-    __shared__ Pieces ps;
-    count_pieces(p, ps);
-    const unsigned per = ps.first[p.n];
+    __shared__ Units us;
+    count_units(p, us);
+    const unsigned per = us.first[p.n];
     unsigned long long lo, hi;
     share((unsigned long long)n * per, lo, hi);
-    for (unsigned long long it = lo; it < hi; ++it) {
-        const int d = idx[it / per];
-        const unsigned q = (unsigned)(it % per);
+    for (unsigned long long it = lo; it < hi;) {
+        const int i = (int)(it / per);
+        const unsigned q = (unsigned)(it - (unsigned long long)i * per);
+        const int d = idx[i];
         if ((unsigned)d >= (unsigned)p.slots) {
             if (d != -1 && q == 0 && threadIdx.x == 0) raise_device_error(p.err, GDR_DEVERR_SLOT_INDEX);
+            it += per - q;
             continue;
         }
         if (live && q == 0 && threadIdx.x == 0) live[d] = 0;
-        move_piece(p, ps, q, -1, d);
+        it += move_units(p, us, q, hi - it, -1, d);
     }
 }
 
@@ -184,8 +194,8 @@ __host__ __device__ constexpr int words_of(int n) { return (n + 31) / 32; }
 __global__ void __launch_bounds__(kThreads) slot_fork_kernel(const SlotPools p, const int32_t *table,
                                                              const int32_t *parents, int n, int32_t *new_table) {
     extern __shared__ unsigned smem[];
-    __shared__ Pieces ps;
-    count_pieces(p, ps);
+    __shared__ Units us;
+    count_units(p, us);
     const int W = words_of(n);
     int *first = reinterpret_cast<int *>(smem);  // the lowest row that continues from row r, n if none
     Bits extra{smem + n, smem + n + W, W};       // rows that take another row's slot
@@ -212,7 +222,7 @@ __global__ void __launch_bounds__(kThreads) slot_fork_kernel(const SlotPools p, 
     count_words(extra);
     count_words(dead);
     // as many rows take another slot as slots are left: n less the rows that are continued
-    const unsigned moves = extra.before[W], per = ps.first[p.n];
+    const unsigned moves = extra.before[W], per = us.first[p.n];
     if (blockIdx.x == gridDim.x - 1)
         for (int i = threadIdx.x; i < n; i += kThreads) {
             const int r = parents[i];
@@ -224,8 +234,8 @@ __global__ void __launch_bounds__(kThreads) slot_fork_kernel(const SlotPools p, 
     long long now = -1;
     int s = -1, d = -1;
     bool go = false;
-    for (unsigned long long it = lo; it < hi; ++it) {
-        const unsigned k = (unsigned)(it / per);
+    for (unsigned long long it = lo; it < hi;) {
+        const unsigned k = (unsigned)(it / per), q = (unsigned)(it - (unsigned long long)k * per);
         if (k != now) {
             now = k;
             const int row = member(dead, k), r = parents[member(extra, k)];
@@ -243,15 +253,15 @@ __global__ void __launch_bounds__(kThreads) slot_fork_kernel(const SlotPools p, 
                 }
             }
         }
-        if (go) move_piece(p, ps, (unsigned)(it % per), s, d);
+        it += go ? move_units(p, us, q, hi - it, s, d) : per - q;
     }
 }
 
 __global__ void __launch_bounds__(kThreads) slot_compact_kernel(const SlotPools p, const int32_t *live,
                                                                 int32_t *new_slot, int32_t *n_live) {
     extern __shared__ unsigned smem[];
-    __shared__ Pieces ps;
-    count_pieces(p, ps);
+    __shared__ Units us;
+    count_units(p, us);
     const int n = p.slots, W = words_of(n);
     Bits used{smem, smem + W, W}, hole{smem + 2 * W + 1, smem + 3 * W + 1, W};
     for (int i0 = 0; i0 < W * 32; i0 += kThreads) {
@@ -267,7 +277,7 @@ __global__ void __launch_bounds__(kThreads) slot_compact_kernel(const SlotPools 
     count_words(hole);
     const int all = (int)used.before[W];
     const int stay = all < n ? rank_of(used, all) : all;  // live slots that are in place already
-    const unsigned moves = (unsigned)(all - stay), per = ps.first[p.n];
+    const unsigned moves = (unsigned)(all - stay), per = us.first[p.n];
     if (blockIdx.x == 0 && threadIdx.x == 0) *n_live = all;
     for (int i = blockIdx.x * kThreads + threadIdx.x; i < n; i += gridDim.x * kThreads) {
         const bool u = used.word[i >> 5] >> (i & 31) & 1;
@@ -275,9 +285,16 @@ __global__ void __launch_bounds__(kThreads) slot_compact_kernel(const SlotPools 
     }
     unsigned long long lo, hi;
     share((unsigned long long)moves * per, lo, hi);
-    for (unsigned long long it = lo; it < hi; ++it) {
-        const unsigned k = (unsigned)(it / per);
-        move_piece(p, ps, (unsigned)(it % per), member(used, stay + k), member(hole, k));
+    long long now = -1;
+    int s = 0, d = 0;
+    for (unsigned long long it = lo; it < hi;) {
+        const unsigned k = (unsigned)(it / per), q = (unsigned)(it - (unsigned long long)k * per);
+        if (k != now) {
+            now = k;
+            s = member(used, stay + k);
+            d = member(hole, k);
+        }
+        it += move_units(p, us, q, hi - it, s, d);
     }
 }
 
@@ -286,16 +303,16 @@ LaunchCache free_cache(reinterpret_cast<const void *>(slot_free_kernel));
 LaunchCache fork_cache(reinterpret_cast<const void *>(slot_fork_kernel));
 LaunchCache compact_cache(reinterpret_cast<const void *>(slot_compact_kernel));
 
-// blocks: all that are resident at once, but no more than there can be work items
+// blocks: all that are resident at once, but no more than there can be units
 cudaError_t grid_for(LaunchCache &c, const SlotPools &p, long long slots, int smem, int *grid) {
     cudaError_t e = c.allow_smem(smem);
     if (e != cudaSuccess) return e;
     e = c.resident_grid(kThreads, smem, grid);
     if (e != cudaSuccess) return e;
     unsigned long long per = 0;
-    for (int i = 0; i < p.n; ++i) per += (p.bytes[i] + kPiece - 1) / kPiece;
-    const unsigned long long items = per * (unsigned long long)slots;
-    if (items < (unsigned long long)*grid) *grid = items > 0 ? (int)items : 1;
+    for (int i = 0; i < p.n; ++i) per += (p.bytes[i] + kUnit - 1) / kUnit;
+    const unsigned long long units = per * (unsigned long long)slots;
+    if (units < (unsigned long long)*grid) *grid = units > 0 ? (int)units : 1;
     return cudaSuccess;
 }
 
