@@ -102,19 +102,23 @@ __device__ __forceinline__ void stage_segment(R (*dst)[kThreads], const void *sr
         for (int j = 0; j < TS; ++j) stage<R, true>(&dst[j][threadIdx.x], j < n ? p + j * (size_t)row : p, j < n);
     }
 }
-// the same for a warp whose lanes lie side by side over 32 * 8 bytes of a row: 16 bytes a lane, two rows an instruction.  p is
-// the row's start at the warp's first channel, `bytes` what the row still holds there (a multiple of 16, may be <= 0).
-// Lanes read what others copied: __syncwarp() after the wait and before the next copy.
-template <int TS, int kThreads>
-__device__ __forceinline__ void stage_rows(uint2 (*dst)[kThreads], const char *p, unsigned row, int n, int bytes) {
-    const int lane = threadIdx.x & 31, sub = lane >> 4, at = (lane & 15) * 16;
+// the same by warps: lx lanes lie side by side over a row's elements of R, and the 32 / lx segments of TS tokens of the warp
+// follow one another, so that 16 bytes a lane cover the same lx * sizeof(R) bytes (at least 16) of one row after the
+// other.  p is the warp's first token's row at the block's first channel, n its valid tokens (may be <= 0), `bytes` what
+// the rows still hold there (a multiple of 16, may be <= 0).  Lanes read what others copied: __syncwarp() after the wait
+// and before the next copy.
+template <int TS, int kThreads, typename R>
+__device__ __forceinline__ void stage_rows(R (*dst)[kThreads], const char *p, unsigned row, int lx, int n, int bytes) {
+    const int lane = threadIdx.x & 31, lanes = lx * (int)sizeof(R) / 16;  // lanes of a row: a power of two
+    const int sub = lane / lanes, at = (lane & (lanes - 1)) * 16, rows = 32 / lanes;
     const bool on = at < bytes;
 #pragma unroll
-    for (int j = 0; j < TS; j += 2) {
-        const bool in = on && j + sub < n;
-        const unsigned d = (unsigned)__cvta_generic_to_shared(&dst[j + sub][threadIdx.x & ~31]) + at;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d),
-                     "l"(in ? p + (j + sub) * (size_t)row + at : p), "r"(in ? 16 : 0)
+    for (int k = 0; k < TS * (int)sizeof(R) / 16; ++k) {
+        const int r = k * rows + sub;  // the warp's token
+        const bool in = on && r < n;
+        const unsigned d = (unsigned)__cvta_generic_to_shared(&dst[r & (TS - 1)][(threadIdx.x & ~31) + r / TS * lx]) + at;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(in ? p + r * (size_t)row + at : p),
+                     "r"(in ? 16 : 0)
                      : "memory");
     }
 }

@@ -10,13 +10,15 @@ namespace gdr {
 namespace {
 using namespace scan;
 
-// kWide: all 32 lanes of a warp lie over the channels, a segment is a warp and no shuffles are needed.  A tile has to hold
-// whole chunks, which it does then with 8 tokens a thread.
-// tokens of a thread in a tile, and blocks of an SM: decays, states and gradients of a segment stay in registers
-template <typename T, bool kMix> constexpr int kStepsOf = sizeof(T) == 2 && !kMix ? 8 : 4;
-template <typename T, bool kMix> constexpr int kBlocksOf = sizeof(T) == 2 && !kMix ? 2 : kMix ? 2 : 3;
+// 8 tokens of 2 channels a thread: decays, states and gradients of a segment, and the mixing form's 1 - a (it cannot be
+// taken from a without losing the digits it has near 0), stay in 128 registers.  Without mixing, 16-bit types take 4
+// channels where a tile is a whole warp wide.  (4 channels everywhere, and 4 tokens where that is too much, spilled: fp16
+// mixing, 128 rows of 128 channels and 4096 tokens, 192 us against 135.)
+constexpr int kSteps = 8;
+constexpr int kResident = 2;  // blocks of an SM
 
-template <typename T, typename G, int V, int kSteps, bool kWide> struct Layout {
+// kWide: all 32 lanes of a warp lie over the channels, a segment is a warp and no shuffles are needed
+template <typename T, typename G, int V, bool kWide> struct Layout {
     static constexpr int kCh = (kWide ? 32 : 16) * V;
     RawV<G, V> g[kSteps][kThreads];
     RawV<T, V> x[kSteps][kThreads], d[kSteps][kThreads];
@@ -26,11 +28,10 @@ template <typename T, typename G, int V, int kSteps, bool kWide> struct Layout {
     uint64_t arrived[2];
 };
 
-template <typename T, typename G, bool kMix, int V, bool kWide>
-__global__ void __launch_bounds__(kThreads, (kBlocksOf<T, kMix>)) scan_bwd_kernel(const ScanBwdArgs a, const Cut cut) {
+template <typename T, typename G, bool kMix, int V, bool kWide, bool kRows>
+__global__ void __launch_bounds__(kThreads, kResident) scan_bwd_kernel(const ScanBwdArgs a, const Cut cut) {
     extern __shared__ __align__(16) unsigned char smem[];
-    constexpr int kSteps = kStepsOf<T, kMix>;
-    auto &sm = *reinterpret_cast<Layout<T, G, V, kSteps, kWide> *>(smem);
+    auto &sm = *reinterpret_cast<Layout<T, G, V, kWide> *>(smem);
     constexpr int P = kPairs<V>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int lx = kWide ? 32 : cut.lx, cl = lane & (lx - 1);
@@ -74,23 +75,21 @@ __global__ void __launch_bounds__(kThreads, (kBlocksOf<T, kMix>)) scan_bwd_kerne
         cluster_meet();
     }
 
-    const int left = kWide ? (a.D - slab * 32 * V) * 2 : 0;  // bytes of a row of 16-bit elements from the slab on
+    const int left = kRows ? a.D - slab * lx * V : 0;  // channels from the slab on
     auto fetch = [&](int k) {
-        const unsigned t0 = k * step + rank * TT + seg * kSteps;
-        const int nt = t0 < L ? (int)min((unsigned)kSteps, L - t0) : 0;
-        const size_t at = nt > 0 ? t0 : 0;
-        if constexpr (kWide && sizeof(G) * V == 8)
-            stage_rows<kSteps>(sm.g, g + at * row_g - lane * 8, row_g, nt, left);
-        else
-            stage_segment<kSteps>(sm.g, g + at * row_g, row_g, on ? nt : 0);
-        if constexpr (kWide && sizeof(T) * V == 8)
-            stage_rows<kSteps>(sm.x, x + at * row_x - lane * 8, row_x, nt, left);
-        else
-            stage_segment<kSteps>(sm.x, x + at * row_x, row_x, on ? nt : 0);
-        if constexpr (kWide && sizeof(T) * V == 8)
-            stage_rows<kSteps>(sm.d, d + at * row_x - lane * 8, row_x, nt, left);
-        else
-            stage_segment<kSteps>(sm.d, d + at * row_x, row_x, on ? nt : 0);
+        const unsigned w0 = k * step + rank * TT + warp * (32 / lx) * kSteps, t0 = k * step + rank * TT + seg * kSteps;
+        const int nw = w0 < L ? (int)min(L - w0, 32u * kSteps) : 0;  // valid tokens of the warp, of the thread
+        const int nt = on && t0 < L ? (int)min((unsigned)kSteps, L - t0) : 0;
+        // by warps where rows are made of whole 16 bytes, but for narrow tiles whose vectors are 16 bytes anyway
+        auto take = [&](auto &dst, const char *src, unsigned row, int size) {
+            if (kRows && (kWide || size * V < 16))
+                stage_rows<kSteps>(dst, src + (nw > 0 ? (size_t)w0 * row : 0) - cl * V * size, row, lx, nw, left * size);
+            else
+                stage_segment<kSteps>(dst, src + (nt > 0 ? (size_t)t0 * row : 0), row, nt);
+        };
+        take(sm.g, g, row_g, (int)sizeof(G));
+        take(sm.x, x, row_x, (int)sizeof(T));
+        take(sm.d, d, row_x, (int)sizeof(T));
         const unsigned chunk = t0 / kChunk;
         const bool has = on && chunk * kChunk < L;
         stage<RawV<float, V>, true>(&sm.h[tid], ck + (has ? (size_t)chunk * a.D : 0), has);
@@ -105,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, (kBlocksOf<T, kMix>)) scan_bwd_kerne
         float2 av[kSteps][P], rest[kMix ? kSteps : 1][P], xv[kSteps][P], A[P], F[P], B[P];
         RawV<T, V> dr[kSteps];
         stage_wait();
-        if (kWide) __syncwarp();
+        if (kRows) __syncwarp();
         float2 h[P];
         unpack<float, V>(sm.h[tid], h);
 #pragma unroll
@@ -131,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, (kBlocksOf<T, kMix>)) scan_bwd_kerne
 #pragma unroll
             for (int i = 0; i < P; ++i) B[i] = __fmul2_rn(av[j][i], j < kSteps - 1 ? __fadd2_rn(dv[i], B[i]) : dv[i]);
         }
-        if (kWide) __syncwarp();
+        if (kRows) __syncwarp();
         if (k > 0) fetch(k - 1);  // what this thread (this warp) copied for itself is in registers
         // over the segments of the warp: (EA, EF) those before this one, (LA, LB) those behind it
         float2 EA[P], EF[P], LA[P], LB[P];
@@ -310,29 +309,29 @@ __global__ void __launch_bounds__(kThreads, (kBlocksOf<T, kMix>)) scan_bwd_kerne
     if (a.dinitial_state && seg == 0 && rank == 0) store<float, V>(a.dinitial_state + (size_t)bn * a.D + c0, mu);
 }
 
-template <typename T, typename G, bool kMix, int V, bool kWide>
+template <typename T, typename G, bool kMix, int V, bool kWide, bool kRows>
 cudaError_t launch_v(const ScanBwdArgs &a, const Cut &cut, cudaStream_t s) {
-    static LaunchCache cache(reinterpret_cast<const void *>(scan_bwd_kernel<T, G, kMix, V, kWide>));
-    const int smem = (int)sizeof(Layout<T, G, V, kStepsOf<T, kMix>, kWide>);
+    static LaunchCache cache(reinterpret_cast<const void *>(scan_bwd_kernel<T, G, kMix, V, kWide, kRows>));
+    const int smem = (int)sizeof(Layout<T, G, V, kWide>);
     const cudaError_t e = cache.allow_smem(smem);
     if (e != cudaSuccess) return e;
-    return launch_clusters(scan_bwd_kernel<T, G, kMix, V, kWide>, (long long)a.B * a.N, cut, smem, a, s);
+    return launch_clusters(scan_bwd_kernel<T, G, kMix, V, kWide, kRows>, (long long)a.B * a.N, cut, smem, a, s);
 }
 
-// vectors of 4 channels where rows are made of whole ones, of 2, else single channels
 template <typename T, typename G, bool kMix> cudaError_t launch_m(const ScanBwdArgs &a, cudaStream_t s) {
-    constexpr int kSteps = kStepsOf<T, kMix>, kMin = 32 * kSteps / kChunk;
-    constexpr bool kCanBeWide = kSteps == 8;
-    const long long rows = (long long)a.B * a.N;
-    constexpr int kResident = kBlocksOf<T, kMix>;
-    if (a.D % 4 == 0) {
-        const Cut cut = choose_cut(rows, a.D, 4, a.S, kSteps, kCanBeWide && wide_rows<T>(a.D) ? 32 : 16, kMin, kResident);
-        if constexpr (kCanBeWide)
-            if (cut.lx == 32) return launch_v<T, G, kMix, 4, true>(a, cut, s);
-        return launch_v<T, G, kMix, 4, false>(a, cut, s);
+    auto cut = [&](int V, int max_lx, int min_lx) {
+        return choose_cut((long long)a.B * a.N, a.D, V, a.S, kSteps, max_lx, min_lx, kResident, 0.78);
+    };
+    if (rows_of_16<T>(a.D)) {
+        const Cut c = cut(2, 32, 4);
+        if constexpr (sizeof(T) == 2 && !kMix) {
+            const Cut c4 = cut(4, 32, 32);
+            if (c4.estimate < 2 * c.estimate) return launch_v<T, G, kMix, 4, true, true>(a, c4, s);
+        }
+        return c.lx == 32 ? launch_v<T, G, kMix, 2, true, true>(a, c, s) : launch_v<T, G, kMix, 2, false, true>(a, c, s);
     }
-    if (a.D % 2 == 0) return launch_v<T, G, kMix, 2, false>(a, choose_cut(rows, a.D, 2, a.S, kSteps, 16, kMin, kResident), s);
-    return launch_v<T, G, kMix, 1, false>(a, choose_cut(rows, a.D, 1, a.S, kSteps, 16, kMin, kResident), s);
+    if (a.D % 2 == 0) return launch_v<T, G, kMix, 2, false, false>(a, cut(2, 16, 4), s);
+    return launch_v<T, G, kMix, 1, false, false>(a, cut(1, 16, 4), s);
 }
 template <typename T, typename G> cudaError_t launch_t(const ScanBwdArgs &a, cudaStream_t s) {
     return a.mode == GDR_SCAN_MIX ? launch_m<T, G, true>(a, s) : launch_m<T, G, false>(a, s);

@@ -1,7 +1,8 @@
 // scan_fwd.cu -- the gated linear recurrence over a sequence (gdr_scan_fwd): h_t = a_t h_{t-1} + b_t per channel, a_t =
 // exp(g_t), b_t = x_t or (1 - a_t) x_t.
 //
-// One pass over x and g (scan_tile.cuh).  The next tile's inputs are on their way (cp.async) while a tile is composed and
+// One pass over x and g (scan_tile.cuh), 8 tokens of 4 channels a thread (fewer channels where rows are not made of
+// whole vectors).  The next tile's inputs are on their way (cp.async) while a tile is composed and
 // written.  Bound by HBM.
 #include "scan_tile.cuh"
 
@@ -21,7 +22,7 @@ template <typename T, typename G, int V, bool kWide> struct Layout {
     uint64_t arrived[2];                                 // their bytes
 };
 
-template <typename T, typename G, bool kMix, int V, bool kWide>
+template <typename T, typename G, bool kMix, int V, bool kWide, bool kRows>
 __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a, const Cut cut) {
     extern __shared__ __align__(16) unsigned char smem[];
     auto &sm = *reinterpret_cast<Layout<T, G, V, kWide> *>(smem);
@@ -66,19 +67,20 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
         cluster_meet();  // every block of the cluster has started, with its barriers ready
     }
 
-    const int left = kWide ? (a.D - slab * 32 * V) * 2 : 0;  // bytes of a row of 16-bit elements from the slab on
+    const int left = kRows ? a.D - slab * lx * V : 0;  // channels from the slab on
     auto fetch = [&](int k) {
-        const unsigned t0 = k * step + rank * TT + seg * kSteps;
-        const int nt = t0 < L ? (int)min((unsigned)kSteps, L - t0) : 0;
-        const size_t at = nt > 0 ? t0 : 0;
-        if constexpr (kWide && sizeof(G) * V == 8)
-            stage_rows<kSteps>(sm.g, g + at * row_g - lane * 8, row_g, nt, left);
-        else
-            stage_segment<kSteps>(sm.g, g + at * row_g, row_g, on ? nt : 0);
-        if constexpr (kWide && sizeof(T) * V == 8)
-            stage_rows<kSteps>(sm.x, x + at * row_x - lane * 8, row_x, nt, left);
-        else
-            stage_segment<kSteps>(sm.x, x + at * row_x, row_x, on ? nt : 0);
+        const unsigned w0 = k * step + rank * TT + warp * (32 / lx) * kSteps, t0 = k * step + rank * TT + seg * kSteps;
+        const int nw = w0 < L ? (int)min(L - w0, 32u * kSteps) : 0;  // valid tokens of the warp, of the thread
+        const int nt = on && t0 < L ? (int)min((unsigned)kSteps, L - t0) : 0;
+        // by warps where rows are made of whole 16 bytes, but for narrow tiles whose vectors are 16 bytes anyway
+        auto take = [&](auto &dst, const char *src, unsigned row, int size) {
+            if (kRows && (kWide || size * V < 16))
+                stage_rows<kSteps>(dst, src + (nw > 0 ? (size_t)w0 * row : 0) - cl * V * size, row, lx, nw, left * size);
+            else
+                stage_segment<kSteps>(dst, src + (nt > 0 ? (size_t)t0 * row : 0), row, nt);
+        };
+        take(sm.g, g, row_g, (int)sizeof(G));
+        take(sm.x, x, row_x, (int)sizeof(T));
         stage_commit();
     };
     if (tiles > 0) fetch(0);
@@ -88,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
         // decays and writes of the segment (tokens behind the sequence: a = 1, b = 0), and the segment as a whole
         float2 av[kSteps][P], bv[kSteps][P], A[P], B[P];
         stage_wait();
-        if (kWide) __syncwarp();
+        if (kRows) __syncwarp();
 #pragma unroll
         for (int j = 0; j < kSteps; ++j) {
             float2 gv[P];
@@ -103,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
                 B[i] = j ? __ffma2_rn(av[j][i], B[i], bv[j][i]) : bv[j][i];
             }
         }
-        if (kWide) __syncwarp();
+        if (kRows) __syncwarp();
         if (k + 1 < tiles) fetch(k + 1);  // what this thread (this warp) copied for itself is in registers
         // inclusive composition over the segments of the warp; (EA, EB): the segments before this one
         float2 EA[P], EB[P];
@@ -228,24 +230,24 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
     if (a.final_state && Lr >= 0 && seg == 0 && rank == 0) store<float, V>(a.final_state + (size_t)bn * a.D + c0, h);
 }
 
-template <typename T, typename G, bool kMix, int V, bool kWide>
+template <typename T, typename G, bool kMix, int V, bool kWide, bool kRows>
 cudaError_t launch_v(const ScanArgs &a, const Cut &cut, cudaStream_t s) {
-    static LaunchCache cache(reinterpret_cast<const void *>(scan_fwd_kernel<T, G, kMix, V, kWide>));
+    static LaunchCache cache(reinterpret_cast<const void *>(scan_fwd_kernel<T, G, kMix, V, kWide, kRows>));
     const int smem = (int)sizeof(Layout<T, G, V, kWide>);
     const cudaError_t e = cache.allow_smem(smem);
     if (e != cudaSuccess) return e;
-    return launch_clusters(scan_fwd_kernel<T, G, kMix, V, kWide>, (long long)a.B * a.N, cut, smem, a, s);
+    return launch_clusters(scan_fwd_kernel<T, G, kMix, V, kWide, kRows>, (long long)a.B * a.N, cut, smem, a, s);
 }
 
-// vectors of 4 channels where rows are made of whole ones, of 2, else single channels
 template <typename T, typename G, bool kMix> cudaError_t launch_m(const ScanArgs &a, cudaStream_t s) {
-    const long long rows = (long long)a.B * a.N;
-    if (a.D % 4 == 0) {
-        const Cut cut = choose_cut(rows, a.D, 4, a.S, kSteps, wide_rows<T>(a.D) ? 32 : 16, 4, 2);
-        return cut.lx == 32 ? launch_v<T, G, kMix, 4, true>(a, cut, s) : launch_v<T, G, kMix, 4, false>(a, cut, s);
+    auto cut = [&](int V, int max_lx) { return choose_cut((long long)a.B * a.N, a.D, V, a.S, kSteps, max_lx, 4, 2, 0.85); };
+    if (rows_of_16<T>(a.D)) {
+        const Cut c = cut(4, 32);
+        return c.lx == 32 ? launch_v<T, G, kMix, 4, true, true>(a, c, s) : launch_v<T, G, kMix, 4, false, true>(a, c, s);
     }
-    if (a.D % 2 == 0) return launch_v<T, G, kMix, 2, false>(a, choose_cut(rows, a.D, 2, a.S, kSteps, 16, 4, 2), s);
-    return launch_v<T, G, kMix, 1, false>(a, choose_cut(rows, a.D, 1, a.S, kSteps, 16, 4, 2), s);
+    if (a.D % 4 == 0) return launch_v<T, G, kMix, 4, false, false>(a, cut(4, 16), s);
+    if (a.D % 2 == 0) return launch_v<T, G, kMix, 2, false, false>(a, cut(2, 16), s);
+    return launch_v<T, G, kMix, 1, false, false>(a, cut(1, 16), s);
 }
 template <typename T, typename G> cudaError_t launch_t(const ScanArgs &a, cudaStream_t s) {
     return a.mode == GDR_SCAN_MIX ? launch_m<T, G, true>(a, s) : launch_m<T, G, false>(a, s);

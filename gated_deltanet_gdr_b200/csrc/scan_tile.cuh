@@ -118,23 +118,24 @@ __device__ __forceinline__ bool wait_remote(uint64_t *bar, unsigned parity, uint
 
 // ---- the cut -------------------------------------------------------------------------------------------------------
 
-// whether 32 lanes may lie over the channels: rows of 16-bit elements are then staged 16 bytes at a time
-template <typename T> bool wide_rows(int D) { return sizeof(T) == 4 || D % 8 == 0; }
+// whether rows are made of whole 16 bytes: tiles are then staged by warps
+template <typename T> bool rows_of_16(int D) { return D * (long long)sizeof(T) % 16 == 0; }
 
 struct Cut {
     int lx;     // lanes side by side over the channels, a power of two from 2 to 32
     int slabs;  // tiles over the channels
     int ranks;  // blocks of a cluster: consecutive tiles in time
+    double estimate;
 };
 
 // The cut of the least estimated time.  A block spends about the same time on every tile, whatever its shape (a little
-// more with fewer lanes, for the shuffles), so a cut costs the tiles that a block walks through, times what the blocks of
+// more with fewer lanes, for the shuffles; `wide` with 32, which need none), so a cut costs the tiles that a block walks through, times what the blocks of
 // the fullest SM cost together: 1 for one, 0.8 more for each of the up to `resident` that share it at a time.  A cluster
 // lies within one of the GPU's groups of SMs, which are not multiples of it: kFit, as the occupancy query reports it.
 // Measured, forward, us: 640 channels and 32769 tokens, 8 lanes: 59 with clusters of 6 (20 of the 22 that fit), 67 of 5, 72 of 8
 // (15 fit), 77 of 7; 128 rows of 128 channels and 4096 tokens: 92 with 32 lanes and 2 blocks, 93 with 16 and 1, 102 with 8 and 1; 64
 // channels and 65536 tokens: 45 with 4 lanes and 8 blocks, 77 with 8 lanes.
-inline Cut choose_cut(long long rows, int D, int V, int S, int TS, int max_lx, int min_lx, int resident) {
+inline Cut choose_cut(long long rows, int D, int V, int S, int TS, int max_lx, int min_lx, int resident, double wide) {
     // clusters of 1 .. 8 blocks that a B200 of 148 SMs holds with one block on an SM
     constexpr int kFit[kMaxRanks] = {148, 74, 45, 33, 26, 22, 15, 15};
     const int sms = sm_count();
@@ -143,20 +144,19 @@ inline Cut choose_cut(long long rows, int D, int V, int S, int TS, int max_lx, i
         return (double)(n / resident) * share(resident) + share(n % resident);
     };
     Cut best{};
-    double least = 0;
     for (int lx = max_lx; lx >= min_lx; lx /= 2) {
         const long long slabs = (D + (long long)lx * V - 1) / ((long long)lx * V), clusters = rows * slabs;
         const long long tile = (long long)TS * (kThreads / lx);
-        const double shuffles = lx == 32 ? 0.85 : lx == 16 ? 0.93 : lx == 8 ? 1.0 : lx == 4 ? 1.11 : 1.25;
+        const double shuffles = lx == 32 ? wide : lx == 16 ? 0.93 : lx == 8 ? 1.0 : lx == 4 ? 1.11 : 1.25;
         for (int r = 1; r <= kMaxRanks && (r == 1 || (r - 1) * tile < S); ++r) {
             const long long fit = kFit[r - 1] * sms >= 148 ? kFit[r - 1] * sms / 148 : 1;
             const double t = shuffles * (1.0 + 0.02 * r) * (double)((S + r * tile - 1) / (r * tile)) *
                              together((clusters + fit - 1) / fit);
-            if (!best.lx || t < least) {
-                least = t;
+            if (!best.lx || t < best.estimate) {
                 best.lx = lx;
                 best.slabs = (int)slabs;
                 best.ranks = r;
+                best.estimate = t;
             }
         }
     }
