@@ -574,6 +574,13 @@ int take_pools(const gdr_pool *pools, int n_pools, int slots, long long max_slot
 }
 
 constexpr long long kMaxSlots = (1LL << 24) - 1;
+
+// whether an array of n words lies in a pool, where a move could change it while it is read
+bool in_pools(const SlotPools &p, const void *a, long long n) {
+    for (int i = 0; i < p.n; ++i)
+        if (overlap({p.data[i], p.bytes[i] * (unsigned long long)p.slots}, {a, 4ull * n})) return true;
+    return false;
+}
 }  // namespace
 
 extern "C" int gdr_slot_copy(const gdr_pool *pools, int n_pools, int slots, const int32_t *src, const int32_t *dst,
@@ -584,6 +591,7 @@ extern "C" int gdr_slot_copy(const gdr_pool *pools, int n_pools, int slots, cons
     if (n < 0 || n > kMaxSlotMoves) return GDR_ERR_SHAPE;
     if (n > 0 && (!src || !dst)) return GDR_ERR_NULL;
     if (!aligned16(src) || !aligned16(dst)) return GDR_ERR_ALIGN;
+    if (in_pools(p, src, n) || in_pools(p, dst, n)) return GDR_ERR_SHAPE;
     if (n == 0) return GDR_OK;
     if ((st = device_setup(&p.err))) return st;
     return launch_slot_copy(p, src, dst, n, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? GDR_OK
@@ -601,6 +609,7 @@ extern "C" int gdr_slot_fork(const gdr_pool *pools, int n_pools, int slots, cons
     // every block reads both inputs while one writes the result
     if (n > 0 && (new_slot_table < slot_table + n && slot_table < new_slot_table + n)) return GDR_ERR_SHAPE;
     if (n > 0 && (new_slot_table < parents + n && parents < new_slot_table + n)) return GDR_ERR_SHAPE;
+    if (in_pools(p, slot_table, n) || in_pools(p, parents, n) || in_pools(p, new_slot_table, n)) return GDR_ERR_SHAPE;
     if (n == 0) return GDR_OK;
     if ((st = device_setup(&p.err))) return st;
     return launch_slot_fork(p, slot_table, parents, n, new_slot_table, reinterpret_cast<cudaStream_t>(stream)) ==
@@ -617,6 +626,7 @@ extern "C" int gdr_slot_compact(const gdr_pool *pools, int n_pools, int slots, c
     if (new_slot < live + slots && live < new_slot + slots) return GDR_ERR_SHAPE;
     if (n_live >= live && n_live < live + slots) return GDR_ERR_SHAPE;
     if (n_live >= new_slot && n_live < new_slot + slots) return GDR_ERR_SHAPE;
+    if (in_pools(p, live, slots) || in_pools(p, new_slot, slots) || in_pools(p, n_live, 1)) return GDR_ERR_SHAPE;
     if ((st = device_setup(&p.err))) return st;
     return launch_slot_compact(p, live, new_slot, n_live, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? GDR_OK : GDR_ERR_LAUNCH;
@@ -631,6 +641,7 @@ extern "C" int gdr_slot_free(const gdr_pool *pools, int n_pools, int slots, cons
     if (n > 0 && !idx) return GDR_ERR_NULL;
     if (!aligned16(idx) || !aligned16(live)) return GDR_ERR_ALIGN;
     if (n > 0 && live && idx < live + slots && live < idx + n) return GDR_ERR_SHAPE;
+    if (in_pools(p, idx, n) || (live && in_pools(p, live, slots))) return GDR_ERR_SHAPE;
     if (n == 0) return GDR_OK;
     if ((st = device_setup(&p.err))) return st;
     return launch_slot_free(p, idx, n, live, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? GDR_OK

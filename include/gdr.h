@@ -440,7 +440,8 @@ int gdr_scan_step(const void *x, const void *g, float *state_pool, int slots, co
  *
  *   data        device, slots * slot_bytes bytes, slot s at data + s * slot_bytes; 16-byte aligned
  *   slot_bytes  bytes of one slot, >= 1 (a multiple of 16 is fastest)
- * The array of gdr_pool is in host memory and is read before the call returns; the pools must not overlap.
+ * The array of gdr_pool is in host memory and is read before the call returns; the pools must not overlap one another or
+ * the index arrays (GDR_ERR_SHAPE).
  */
 #define GDR_MAX_POOLS 64
 typedef struct gdr_pool {

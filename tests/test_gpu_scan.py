@@ -228,6 +228,105 @@ def test_prepared_calls():
     assert torch.equal(out, gdr.scan_fwd(tx, tg, st)[0])
 
 
+@pytest.mark.parametrize("seed", range(40))
+def test_random_cases(seed):
+    r = np.random.default_rng(9000 + seed)
+    dt, gt = TYPES[r.integers(len(TYPES))]
+    B, N, D = int(r.integers(1, 5)), int(r.integers(1, 4)), int(np.exp(r.uniform(0, np.log(400))))
+    S = int(np.exp(r.uniform(0, np.log(1200))))
+    if r.random() < 0.5:
+        D = max(8, D // 8 * 8)
+    run_both(B, N, S, D, dt, gt, bool(r.integers(2)), bool(r.integers(2)), bool(r.integers(2)), 9100 + seed,
+             dfinal=bool(r.integers(2)))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_state_and_gradient_in_place_with_clusters(dt):
+    """final_state over initial_state and dinitial_state over dfinal_state where several blocks share a sequence, with an
+    empty sequence and one that ends inside a tile."""
+    B, N, S, D = 3, 1, 5000, 64
+    x, g, s0, r = draws(B, N, S, D, dt, "f32", 580)
+    L = np.array([5000, 0, 3333], np.int32)
+    tx, tg, st = spoil(dev(x, dt), L), spoil(dev(g, "f32"), L), dev(s0, "f32")
+    df = dev(rnd(r.normal(size=(B, N, D)), "f32"), "f32")
+    out, fin, ck = gdr.scan_fwd(tx, tg, st.clone(), dev_i32(L), output_checkpoints=True)
+    dout = spoil(dev(rnd(r.normal(size=x.shape), dt), dt), L)
+    want = gdr.scan_bwd(tx, tg, ck, dout, df.clone(), dev_i32(L))
+    o, f, _ = gdr.scan_fwd(tx, tg, st, dev_i32(L), final_state=st)
+    got = gdr.scan_bwd(tx, tg, ck, dout, df, dev_i32(L), dinitial_state=df)
+    assert f is st and got[2] is df and gdr.get_error() == 0
+    for u, v in zip((o, f) + got, (out, fin) + want):
+        assert torch.equal(u, v)
+    _, rf, _ = R.scan_fwd(x, g, s0, L)
+    E, _ = scan_bounds(x, g, s0, L, False)
+    check(fin, rf, E[:, :, -1], "f32", "final_state")
+
+
+def test_offsets_past_32_bits():
+    """A tensor of more than 2^32 elements: behind a forgetting gate the end equals a call on the end alone."""
+    S, D, tail = 131200, 32768, 100
+    x = torch.full((1, 1, S, D), 0.25, dtype=torch.bfloat16, device="cuda")
+    x[:, :, -tail:].normal_()
+    g = torch.full((1, 1, S, D), -0.5, dtype=torch.bfloat16, device="cuda")
+    g[:, :, -tail] = float("-inf")
+    out, fin, ck = gdr.scan_fwd(x, g, output_checkpoints=True)
+    xs, gs = x[:, :, -tail:].contiguous(), g[:, :, -tail:].contiguous()
+    o, f, _ = gdr.scan_fwd(xs, gs)
+    ro, rf, _ = R.scan_fwd(host(xs[..., :64]), host(gs[..., :64]))
+    E, _ = scan_bounds(host(xs[..., :64]), host(gs[..., :64]), None, [tail], False)
+    check(out[:, :, -tail:, :64], ro, E[:, :, 1:], "bf16", "out")
+    check(fin[..., :64], rf, E[:, :, -1], "f32", "final_state")
+    # the tiles lie otherwise in the short call, so sums are grouped otherwise: half a bf16 step apart at most, twice
+    assert (out[:, :, -tail:].float() - o.float()).abs().max() <= 2 ** -7 * o.float().abs().max()
+    # a constant input settles at x / (1 - a)
+    assert abs(float(out[0, 0, -tail - 1, -1]) - 0.25 / (1 - np.exp(-0.5))) < 2 ** -8
+    del out, o
+    dx, dg, di = gdr.scan_bwd(x, g, ck, x)
+    assert gdr.get_error() == 0
+    a = np.exp(-0.5)
+    assert abs(float(dx[0, 0, S // 2, -1]) - 0.25 / (1 - a)) < 2 ** -8
+    assert abs(float(di[0, 0, -1]) - 0.25 * a / (1 - a)) < 1e-5
+    assert not torch.any(dg[0, 0, -tail])  # nothing passes a forgotten state
+
+
+@pytest.mark.timeout(300)
+def test_two_host_threads_on_streams_of_their_own():
+    import threading
+    x, g, s0, _ = draws(2, 2, 1500, 128, "bf16", "f32", 590)
+    tx, tg, st = dev(x, "bf16"), dev(g, "f32"), dev(s0, "f32")
+    want = gdr.scan_fwd(tx, tg, st, output_checkpoints=True)
+    wg = gdr.scan_bwd(tx, tg, want[2], tx, st)
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(30):
+                o = gdr.scan_fwd(tx, tg, st, output_checkpoints=True)
+                b = gdr.scan_bwd(tx, tg, o[2], tx, st)
+                if not all(torch.equal(u, v) for u, v in zip(o + b, want + wg)):
+                    bad.append(1)
+
+    ts = [threading.Thread(target=work) for _ in range(2)]
+    [t.start() for t in ts]
+    [t.join() for t in ts]
+    assert not bad and gdr.get_error() == 0
+
+
+def test_step_for_more_sequences_than_a_grid_dimension():
+    B = 70001
+    x = torch.randn(B, 1, 1, 4, device="cuda")
+    g = -torch.rand(B, 1, 1, 4, device="cuda")
+    pool = torch.randn(B + 1, 1, 4, device="cuda")
+    want = torch.exp(g.double())[:, :, 0] * pool[1:].double() + x.double()[:, :, 0]
+    idx = torch.arange(1, B + 1, device="cuda", dtype=torch.int32)
+    out, _ = gdr.scan_step(x, g, pool, idx)
+    # one exponential (4 u), a product and a sum: 6 u of |a h| + |x|
+    tol = 6 * 2.0 ** -24 * (torch.exp(g.double())[:, :, 0] * 8 + x.double().abs()[:, :, 0])
+    assert bool(((pool[1:].double() - want).abs() <= tol).all()) and torch.equal(out[:, :, 0], pool[1:])
+
+
 @pytest.mark.parametrize("dt,gt", TYPES)
 @pytest.mark.parametrize("S,per_token", [(1, False), (1, True), (4, False), (5, True), (8, True)])
 @pytest.mark.parametrize("N,D", [(2, 128), (3, 5)])

@@ -70,6 +70,8 @@ def test_scan_sizes_types_and_modes(L, f):
 
 
 def test_scan_buffers(L):
+    assert fwd(L, B=1, N=1, D=(1 << 26) + 1) == gdr.GDR_ERR_SHAPE
+    assert bwd(L, B=1, N=1, D=(1 << 26) + 1) == gdr.GDR_ERR_SHAPE
     assert fwd(L, out=NUL) == gdr.GDR_ERR_NULL
     assert fwd(L, out=at(0)) == gdr.GDR_ERR_SHAPE  # in place
     assert fwd(L, out=ctypes.c_void_p((2 << 30) + 64)) == gdr.GDR_ERR_SHAPE  # inside g
@@ -138,6 +140,7 @@ def test_slots(L):
             assert f(n=-1) == gdr.GDR_ERR_SHAPE, name
             assert f(n=65537) == gdr.GDR_ERR_SHAPE, name
             assert f(n=0) == gdr.GDR_OK, name
+        assert f(p=pool((1 << 30, 64))) == gdr.GDR_ERR_SHAPE, name  # the first index array lies in the pool
     assert calls["copy"](b=NUL) == gdr.GDR_ERR_NULL
     assert calls["fork"](n=16385) == gdr.GDR_ERR_SHAPE
     assert calls["fork"](c=at(0)) == gdr.GDR_ERR_SHAPE
