@@ -231,22 +231,35 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, K>)) conv1d_bwd_kernel(c
     }
 }
 
-// adds the partial sums of all blocks: 32 channels of one tap a block, its 32 warps each a stride of the rows
-__global__ void __launch_bounds__(1024) conv1d_bwd_sum_kernel(const float *partial, int rows, int C, int K, float *dw,
-                                                              float *db) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane, j = blockIdx.y;
-    float s = 0.f;
-    if (c < C)
-        for (int r = warp; r < rows; r += 32) s += partial[((size_t)r * (K + 1) + j) * C + c];
+// Adds the partial sums of all blocks: 32 channels of one tap a block, 8 lanes of 4 channels beside one another and 32
+// strides of the rows.  It may be launched while the kernel before it still runs, and waits for its end.
+constexpr int kSumThreads = 256;
+__global__ void __launch_bounds__(kSumThreads) conv1d_bwd_sum_kernel(const float *partial, int rows, int C, int K, float *dw,
+                                                                     float *db) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int group = threadIdx.x & 7, stride = threadIdx.x >> 3;
+    const int c = blockIdx.x * 32 + group * 4, j = blockIdx.y;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < C)  // C is a multiple of 16
+        for (int r = stride; r < rows; r += 32) {
+            const float4 v = *reinterpret_cast<const float4 *>(partial + ((size_t)r * (K + 1) + j) * C + c);
+            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+        }
     __shared__ float part[32][33];
-    part[warp][lane] = s;
+    part[stride][group * 4] = s.x;
+    part[stride][group * 4 + 1] = s.y;
+    part[stride][group * 4 + 2] = s.z;
+    part[stride][group * 4 + 3] = s.w;
     __syncthreads();
-    s = warp_sum(part[lane][warp]);  // this warp: channel blockIdx.x * 32 + warp
-    const int cw = blockIdx.x * 32 + warp;
-    if (lane == 0 && cw < C) {
-        if (j < K) dw[(size_t)cw * K + j] = s;
-        else if (db) db[cw] = s;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int cw = warp * 4 + k, at = blockIdx.x * 32 + cw;
+        const float t = warp_sum(part[lane][cw]);
+        if (lane == 0 && at < C) {
+            if (j < K) dw[(size_t)at * K + j] = t;
+            else if (db) db[at] = t;
+        }
     }
 }
 
@@ -279,9 +292,17 @@ cudaError_t launch_tk(const ConvBwdArgs &a, cudaStream_t s) {
     conv1d_bwd_kernel<T, K><<<dim3(gx, gy, a.B), kThreads, smem, s>>>(a, sub);
     e = cudaGetLastError();
     if (e != cudaSuccess || !a.partial) return e;
-    conv1d_bwd_sum_kernel<<<dim3((unsigned)((a.C + 31) / 32), K + 1), 1024, 0, s>>>(a.partial, (int)(a.B * gy), a.C, K,
-                                                                                 a.dw, a.db);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((a.C + 31) / 32), K + 1);
+    cfg.blockDim = dim3(kSumThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, conv1d_bwd_sum_kernel, static_cast<const float *>(a.partial), (int)(a.B * gy), a.C, K, a.dw,
+                              a.db);
 }
 
 template <typename T>
