@@ -3,7 +3,7 @@
 // pre[u] = bias + sum_j w_j x[u - K + 1 + j];  dpre[u] = dy[u] silu'(pre[u]);
 // dx[t] = sum_j w_j dpre[t + K - 1 - j];  dw_j = sum_u dpre[u] x[u - K + 1 + j];  db = sum_u dpre[u].
 //
-// One thread owns 4 channels and walks up to 64 tokens and the K - 1 behind them (whose dpre reaches back into its tokens),
+// One thread owns 4 channels and walks up to 128 tokens and the K - 1 behind them (whose dpre reaches back into its tokens),
 // with a window of the last K inputs and of the last K dpre in registers.  The forward pass is computed again on the
 // way, so x and dy are read and dx written once, apart from the K - 1 tokens at either end, which the neighbouring warps
 // of the block read too.  Tokens come in batches of kBatch through a two-stage ring in shared memory (cp.async, every
@@ -18,7 +18,8 @@ namespace {
 
 constexpr int kWarps = 4;             // warps of a block, adjacent in time
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxSub = 64;           // most tokens that a warp walks, which bounds the terms of a thread's sums
+// most tokens that a warp walks, which bounds the terms of a thread's sums
+template <typename T> constexpr int kMaxSub = sizeof(T) == 2 ? 128 : 64;
 constexpr int kBatch = 8;             // tokens of a stage
 constexpr int V = 4;                  // channels of a thread
 constexpr int P = V / 2;
@@ -268,16 +269,17 @@ __global__ void zero_f32_kernel(float *p, size_t n) {
     if (i < n) p[i] = 0.f;
 }
 
-// Tokens a warp walks: 64, or fewer (down to 16) where blocks of 64 would not even give every SM one -- the walk is the
-// call's latency then, and the K - 1 tokens read twice cost nothing (1 x 4096 tokens, 384 channels, bf16:
-// 16 us with 32 tokens, 20 with 64)
-int sub_for(int B, int S, int C) {
-    int sub = kMaxSub;
+// Tokens a warp walks: as many as pay for its beginning (4 x 4096 tokens of 8192 channels, us: bf16 168 with 128 tokens and 174
+// with 64, fp32 256 and 246).  Fewer, down to 16, where the blocks would not give every SM two -- the walk is the call's latency then, and the K - 1 tokens read twice cost
+// nothing (1 x 4096 tokens of 384 channels: 14 us with 32, 20 with 64) -- or where that leaves fewer warps without tokens.
+int sub_for(int B, int S, int C, int most) {
     const long long groups = (long long)B * ((C + 32 * V - 1) / (32 * V));
-    while (sub > 16 && groups * ((S + (long long)kWarps * sub - 1) / (kWarps * sub)) < sm_count()) sub /= 2;
+    auto blocks = [&](int sub) { return (S + (long long)kWarps * sub - 1) / (kWarps * sub); };
+    int sub = most;
+    while (sub > 16 && (groups * blocks(sub) < 2 * sm_count() || blocks(sub / 2) * 9 <= blocks(sub) * 16)) sub /= 2;
     return sub;
 }
-// blocks along the tokens: at most 65535, since S <= 65535 * 64 and fewer tokens a warp come with fewer blocks
+// blocks along the tokens: at most 65535, of at least 64 tokens each, since S <= 65535 * 64
 int tiles(int S, int sub) { return (int)((S + (long long)kWarps * sub - 1) / (kWarps * sub)); }
 
 template <typename T, int K>
@@ -287,7 +289,7 @@ cudaError_t launch_tk(const ConvBwdArgs &a, cudaStream_t s) {
     cudaError_t e = cache.allow_smem(smem);
     if (e != cudaSuccess) return e;
     const unsigned gx = (unsigned)((a.C + 32 * V - 1) / (32 * V));
-    const int sub = sub_for(a.B, a.S, a.C);
+    const int sub = sub_for(a.B, a.S, a.C, kMaxSub<T>);
     const unsigned gy = (unsigned)(a.S > 0 ? tiles(a.S, sub) : 1);  // without tokens, the state's gradient alone
     conv1d_bwd_kernel<T, K><<<dim3(gx, gy, a.B), kThreads, smem, s>>>(a, sub);
     e = cudaGetLastError();
@@ -323,7 +325,7 @@ cudaError_t launch_t(const ConvBwdArgs &a, int K, cudaStream_t s) {
 }  // namespace
 
 size_t conv1d_bwd_workspace(int B, int S, int C, int K) {
-    return (size_t)B * tiles(S, sub_for(B, S, C)) * (K + 1) * C * sizeof(float);
+    return (size_t)B * tiles(S, sub_for(B, S, C, kMaxSub<float>)) * (K + 1) * C * sizeof(float);  // the most of any type
 }
 
 cudaError_t launch_conv1d_bwd(const ConvBwdArgs &a, int K, gdr_dtype dt, cudaStream_t s) {

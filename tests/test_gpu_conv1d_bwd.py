@@ -3,7 +3,7 @@
 Bounds, with u = 2^-24: pre is a sum of K + 1 terms, off by d1 = (K + 1) u (|bias| + sum |w x|); s = 1 / (1 + e^{-pre}) is
 good to 6 u and silu' = s (1 + pre (1 - s)) to (12 + 8 |pre|) u; its slope is at most 1/2.  So dpre is off by
 e = |dy| (d1 / 2 + (12 + 8 |pre|) u).  dx: sum |w| e plus (K + 1) u of the absolute sum.  dweight, dbias: sum |x| e plus one
-u of the absolute sum for each addition on the way: at most 64 in a thread, 4 over a block's warps, one for each 32nd of the
+u of the absolute sum for each addition on the way: at most 128 in a thread, 4 over a block's warps, one for each 32nd of the
 blocks' sums and 6 more.
 """
 import numpy as np
@@ -37,7 +37,7 @@ def bounds(x, w, bias, state, lengths, dy):
     B, S, C = x.shape
     K = w.shape[1]
     bx, bw, bb, bs = np.zeros((B, S, C)), np.zeros((C, K)), np.zeros(C), np.zeros((B, C, K))
-    adds = (64 + 4 + 6 + -(-B * -(-max(S, 1) // 256) // 32)) * U
+    adds = (128 + 4 + 6 + -(-B * -(-max(S, 1) // 64) // 32)) * U  # a block has at least 64 tokens
     for b in range(B):
         L = int(lengths[b])
         hist = np.zeros((K + L, C))
