@@ -29,7 +29,8 @@
  *     h / (Nv / Nk) (contiguous groups, the repeat_interleave grouping).
  *   - dtype names the type of q, k, v, beta, the state and out: GDR_F32,
  *     GDR_BF16 or GDR_F16 (the chunk_gated_delta_rule operator lists fp16 and
- *     bf16 inputs).  g, gk and the prologue's a, A_log, dt_bias are always fp32.
+ *     bf16 inputs).  g, gk and the prologue's a, A_log, dt_bias are always fp32 (gdr_scan_* also
+ *     take g in dtype, and any N and D).
  *     bf16 and fp16 prefill with Dk = Dv = 128 run on the tensor cores (fp32
  *     accumulation and state, MMA operand copies in the input type); other
  *     head sizes and fp32 run the CUDA-core kernel (fp32 arithmetic, one
