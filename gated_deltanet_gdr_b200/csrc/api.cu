@@ -557,7 +557,8 @@ int take_pools(const gdr_pool *pools, int n_pools, int slots, long long max_slot
     for (int i = 0; i < n_pools; ++i) {
         if (!pools[i].data) return GDR_ERR_NULL;
         if (!aligned16(pools[i].data)) return GDR_ERR_ALIGN;
-        if (pools[i].slot_bytes < 1 || pools[i].slot_bytes > (1ull << 38)) return GDR_ERR_SHAPE;
+        // (the kernels count the units of 4 KB of a slot of all pools in 32 bits)
+        if (pools[i].slot_bytes < 1 || pools[i].slot_bytes > (1ull << 37)) return GDR_ERR_SHAPE;
         out->data[i] = static_cast<char *>(pools[i].data);
         out->bytes[i] = pools[i].slot_bytes;
     }

@@ -30,7 +30,6 @@ template <> struct Raw<8> { using type = uint2; };
 template <> struct Raw<16> { using type = uint4; };
 template <typename T, int V> using RawV = typename Raw<(int)sizeof(T) * V>::type;
 
-
 template <typename T, int V> __device__ __forceinline__ void unpack(const RawV<T, V> &r, float2 (&x)[kPairs<V>]) {
     const T *e = reinterpret_cast<const T *>(&r);
 #pragma unroll
@@ -55,7 +54,7 @@ template <int P> __device__ __forceinline__ void fill(float2 (&x)[P], float v) {
 #pragma unroll
     for (int i = 0; i < P; ++i) x[i] = both(v);
 }
-// pair x from the lane `d` below (or above: the shuffles of a pair are two)
+// a pair from the lane d below, d above
 __device__ __forceinline__ float2 shfl_up2(float2 x, int d) {
     float lo, hi;
     up2(x, lo, hi);

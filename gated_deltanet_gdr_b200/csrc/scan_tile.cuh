@@ -66,6 +66,7 @@ __device__ __forceinline__ int seq_len(const int32_t *lengths, int b, int S) {
 
 // every thread of every block of the cluster passes together; orders no memory but mbarrier initialisations fenced before
 __device__ __forceinline__ void cluster_meet() {
+    __syncwarp();  // the barrier is for whole warps, whose lanes may have left a wait apart
     asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 // writes V floats at `p` and their bytes to the count of `bar` (both given as this block's addresses) in block `rank`

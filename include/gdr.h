@@ -29,8 +29,8 @@
  *     h / (Nv / Nk) (contiguous groups, the repeat_interleave grouping).
  *   - dtype names the type of q, k, v, beta, the state and out: GDR_F32,
  *     GDR_BF16 or GDR_F16 (the chunk_gated_delta_rule operator lists fp16 and
- *     bf16 inputs).  g, gk and the prologue's a, A_log, dt_bias are always fp32 (gdr_scan_* also
- *     take g in dtype, and any N and D).
+ *     bf16 inputs).  g, gk and the prologue's a, A_log, dt_bias are always fp32
+ *     (gdr_scan_* also take g in dtype, and any N and D).
  *     bf16 and fp16 prefill with Dk = Dv = 128 run on the tensor cores (fp32
  *     accumulation and state, MMA operand copies in the input type); other
  *     head sizes and fp32 run the CUDA-core kernel (fp32 arithmetic, one
@@ -89,8 +89,8 @@ typedef enum gdr_dtype { GDR_F32 = 0, GDR_BF16 = 1, GDR_F16 = 2 } gdr_dtype;
 #define GDR_DEVERR_SLOT_INDEX 0x1u /* a referenced slot index was outside [0, slots), or the slot operators'
                                       targets collided */
 #define GDR_DEVERR_LENGTH 0x2u     /* a length was outside [0, S] */
-#define GDR_DEVERR_TIMEOUT 0x4u    /* a kernel's bounded wait for its own copies or for another of its warp
-                                      groups ran out: it released what it held and returned early, so the
+#define GDR_DEVERR_TIMEOUT 0x4u    /* a kernel's bounded wait for its own copies, for another of its warp
+                                      groups or for another block of its cluster ran out: it released what it held and returned early, so the
                                       call's outputs are incomplete (not expected in normal operation) */
 
 /*
@@ -440,7 +440,7 @@ int gdr_scan_step(const void *x, const void *g, float *state_pool, int slots, co
  * layers).
  *
  *   data        device, slots * slot_bytes bytes, slot s at data + s * slot_bytes; 16-byte aligned
- *   slot_bytes  bytes of one slot, >= 1 (a multiple of 16 is fastest)
+ *   slot_bytes  bytes of one slot, 1 .. 2^37 (a multiple of 16 is fastest)
  * The array of gdr_pool is in host memory and is read before the call returns; the pools must not overlap one another or
  * the index arrays (GDR_ERR_SHAPE).
  */
@@ -526,8 +526,8 @@ int gdr_prologue_apply(const void *q, const void *k, const void *b, const float 
 int gdr_get_error(gdr_stream_t stream, int *device_error);
 
 /*
- * Diagnostic hook for the bounded waits of the tensor-core prefill and of the
- * D = 128 decode kernel: their limit in nanoseconds for the calls that follow in
+ * Diagnostic hook for the bounded waits of the tensor-core prefill, of the
+ * D = 128 decode kernel and of the recurrence's clusters: their limit in nanoseconds for the calls that follow in
  * this process (0 restores the default of one second).  A limit shorter than a
  * kernel needs makes its waits run out: the kernel then drains its own copies
  * (and MMAs), returns early and sets GDR_DEVERR_TIMEOUT (outputs and, for

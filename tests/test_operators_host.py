@@ -135,6 +135,7 @@ def test_slots(L):
         assert f(p=pool((None, 64))) == gdr.GDR_ERR_NULL, name
         assert f(p=pool(((1 << 40) + 8, 64))) == gdr.GDR_ERR_ALIGN, name
         assert f(p=pool((1 << 40, 0))) == gdr.GDR_ERR_SHAPE, name
+        assert f(p=pool((1 << 40, (1 << 37) + 1))) == gdr.GDR_ERR_SHAPE, name
         assert f(p=pool((1 << 40, 64), ((1 << 40) + 128, 64)), k=2) == gdr.GDR_ERR_SHAPE, name  # they overlap
         if name != "compact":
             assert f(n=-1) == gdr.GDR_ERR_SHAPE, name
