@@ -57,6 +57,7 @@ class GdrEpilogueStruct(ctypes.Structure):
 
 
 _lib = None
+_quick = None  # the compiled marshalling of the short calls, once the library is loaded (see below)
 _lock = threading.Lock()
 
 
@@ -123,8 +124,24 @@ def lib() -> ctypes.CDLL:
         L.gdr_status_string.argtypes = [i32]
         L.gdr_version.restype = i32
         L.gdr_version.argtypes = []
+        _load_marshal(L)
         _lib = L
         return L
+
+
+def _load_marshal(L) -> None:
+    """Loads _marshal.so and gives it the addresses of the C entries.  Without it (another torch than it was compiled
+    against, say) the short calls are marshalled in Python: the same checks and the same kernels, some microseconds
+    later."""
+    global _quick
+    try:
+        from . import _marshal as m
+    except ImportError:
+        return
+    entries = ("gdr_scan_fwd", "gdr_scan_bwd", "gdr_scan_step", "gdr_conv1d_bwd", "gdr_conv1d_bwd_workspace",
+               "gdr_slot_copy", "gdr_slot_fork", "gdr_slot_compact", "gdr_slot_free")
+    m.bind(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in entries))
+    _quick = m
 
 
 @dataclass
@@ -445,13 +462,28 @@ def prepare_conv1d(x, weight, bias=None, conv_state=None, actual_seq_lengths=Non
 # ---- the conv1d's gradient, the gated linear recurrence and the state slots -------------------------------------
 #
 # These calls marshal for short kernels (a decode step, a handful of slots), where a microsecond of checks is a
-# measurable share: each looks at the current device and stream once, checks a tensor in one expression (``_dev`` names
+# measurable share.  The ordinary case (dense tensors on the current device, the current stream) is checked and marshalled
+# in C++ (csrc/marshal.cpp), which answers None to anything else.  The functions below then say what is wrong, or make
+# the call on another stream: each looks at the current device and stream once, checks a tensor in one expression (``_dev`` names
 # what is wrong with it only when something is), and passes plain integers to the C entry.  With ``stream=`` another than
 # the current stream, the tensors a call allocates belong to that stream, and the allocator is told which streams use what.
 
 _CODES = {torch.float32: GDR_F32, torch.bfloat16: GDR_BF16, torch.float16: GDR_F16}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _ready():
+    """Whether the compiled marshalling is there, after loading the library."""
+    if _lib is None:
+        lib()
+    return _quick
+
+
+def _result(r, what):
+    if type(r) is int:  # a status
+        _check(r, what)
+    return r
 
 
 class _Call:
@@ -549,6 +581,12 @@ def scan_fwd(x, g, initial_state=None, actual_seq_lengths=None, *, mix: bool = F
     x (B, N, S, D) in fp32, bf16 or fp16, g (B, N, S, D) log-decay in fp32 or the dtype of x, initial_state fp32
     (B, N, D) or None.  Returns (out, final_state or None, checkpoints or None); ``output_checkpoints`` keeps the fp32
     states that ``scan_bwd`` needs.  ``final_state`` may be ``initial_state`` (in-place update)."""
+    if stream is None and (_quick or _ready()):
+        dev = torch.cuda.current_device()
+        r = _quick.scan_fwd(x, g, initial_state, actual_seq_lengths, out, final_state, checkpoints, bool(mix),
+                              bool(output_final_state), bool(output_checkpoints), dev, _raw_stream(dev))
+        if r is not None:
+            return _result(r, "gdr_scan_fwd")
     c, args, res = _scan_fwd_args(x, g, initial_state, actual_seq_lengths, mix, out, final_state, output_final_state,
                                   checkpoints, output_checkpoints, stream)
     c.done((_lib or lib()).gdr_scan_fwd(*args), "gdr_scan_fwd")
@@ -569,6 +607,12 @@ def scan_bwd(x, g, checkpoints, dout, dfinal_state=None, actual_seq_lengths=None
              dg=None, dinitial_state=None, output_dinitial_state: bool = True, stream=None):
     """Gradient of ``scan_fwd`` (``gdr_scan_bwd``) from the checkpoints it kept, for the gradients dout (B, N, S, D) of
     out and dfinal_state (B, N, D) of final_state.  Returns (dx, dg, dinitial_state or None)."""
+    if stream is None and (_quick or _ready()):
+        dev = torch.cuda.current_device()
+        r = _quick.scan_bwd(x, g, checkpoints, dout, dfinal_state, actual_seq_lengths, dx, dg, dinitial_state, bool(mix),
+                              bool(output_dinitial_state), dev, _raw_stream(dev))
+        if r is not None:
+            return _result(r, "gdr_scan_bwd")
     B, N, S, D = _sizes(x, "x")
     dt, code = x.dtype, _code(x.dtype)
     gcode = _gate_code(x, g)
@@ -615,6 +659,12 @@ def scan_step(x, g, state_pool, ssm_state_indices, actual_seq_lengths=None, num_
               mix: bool = False, out=None, per_token: bool = False, stream=None):
     """The recurrence for decode over a pool of fp32 states (slots, N, D) (``gdr_scan_step``), updating it in place:
     x, g (B, N, S, D) with S <= 8, index and length arrays as in ``recurrent_step``.  Returns (out, state_pool)."""
+    if stream is None and (_quick or _ready()):
+        dev = torch.cuda.current_device()
+        r = _quick.scan_step(x, g, state_pool, ssm_state_indices, actual_seq_lengths, num_accepted_tokens, out, bool(mix),
+                               bool(per_token), dev, _raw_stream(dev))
+        if r is not None:
+            return _result(r, "gdr_scan_step")
     c, args, res = _scan_step_args(x, g, state_pool, ssm_state_indices, actual_seq_lengths, num_accepted_tokens, mix,
                                    out, per_token, stream)
     c.done((_lib or lib()).gdr_scan_step(*args), "gdr_scan_step")
@@ -640,6 +690,12 @@ def conv1d_bwd(x, weight, dq, dk, dv, bias=None, conv_state=None, actual_seq_len
     """Gradient of ``conv1d`` (``gdr_conv1d_bwd``) for the gradients dq, dk (B, Nk, S, Dk) and dv (B, Nv, S, Dv) of its
     outputs and dconv_state_out (B, C, K) or None of its new state.  Returns (dx (B, S, C), dweight fp32 (C, K), dbias
     fp32 (C,), dconv_state (B, C, K)); ``workspace`` (uint8) is allocated per call when not given."""
+    if stream is None and (_quick or _ready()):
+        dev = torch.cuda.current_device()
+        r = _quick.conv1d_bwd(x, weight, dq, dk, dv, bias, conv_state, actual_seq_lengths, dconv_state_out, dx, dweight, dbias,
+                                dconv_state, workspace, dev, _raw_stream(dev))
+        if r is not None:
+            return _result(r, "gdr_conv1d_bwd")
     if not isinstance(x, torch.Tensor) or x.dim() != 3 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("x must be (B, S, C) and weight (C, K)")
     B, S, C = x.shape
@@ -700,6 +756,11 @@ def slot_copy(pools, src, dst, *, stream=None):
     """pool[dst[i]] = pool[src[i]] in every pool (``gdr_slot_copy``).  ``pools``: one tensor (slots, ...) or a list of
     up to 64 of any types with the same number of slots; src, dst int32 (n), -1 for no move.  A move whose target is
     another move's source or an earlier move's target is skipped and flagged (``get_error``).  Returns pools."""
+    if stream is None and (_quick or _ready()):
+        dev = torch.cuda.current_device()
+        r = _quick.slot_copy(pools, src, dst, dev, _raw_stream(dev))
+        if r is not None:
+            return _result(r, "gdr_slot_copy")
     c = _Call(stream)
     arr, n_pools, slots = _pools(c, pools)
     ps = _list_i32(c, src, "src")
@@ -712,6 +773,11 @@ def slot_fork(pools, slot_table, parents, *, new_slot_table=None, stream=None):
     """Beam reordering (``gdr_slot_fork``): row i continues from row parents[i] (-1: from nothing).  The lowest
     child of a row keeps its slot, the others get copies in the slots of the rows without a child.  Returns the
     new slot of every row (int32)."""
+    if stream is None and (_quick or _ready()):
+        dev = torch.cuda.current_device()
+        r = _quick.slot_fork(pools, slot_table, parents, new_slot_table, dev, _raw_stream(dev))
+        if r is not None:
+            return _result(r, "gdr_slot_fork")
     c = _Call(stream)
     arr, n_pools, slots = _pools(c, pools)
     pt = _list_i32(c, slot_table, "slot_table")
@@ -727,6 +793,11 @@ def slot_compact(pools, live, *, new_slot=None, n_live=None, stream=None):
     """Moves the live slots (live int32 (slots), non-zero) at or above their count into the free slots below it
     (``gdr_slot_compact``).  Returns (new_slot int32 (slots): where each slot went, -1 for free ones; n_live int32
     (1,))."""
+    if stream is None and (_quick or _ready()):
+        dev = torch.cuda.current_device()
+        r = _quick.slot_compact(pools, live, new_slot, n_live, dev, _raw_stream(dev))
+        if r is not None:
+            return _result(r, "gdr_slot_compact")
     c = _Call(stream)
     arr, n_pools, slots = _pools(c, pools)
     pl = _list_i32(c, live, "live", slots)
@@ -740,6 +811,11 @@ def slot_compact(pools, live, *, new_slot=None, n_live=None, stream=None):
 def slot_free(pools, idx, live=None, *, stream=None):
     """Sets the slots idx (int32 (n), -1 for none) of every pool to zero and, with ``live``, marks them free
     (``gdr_slot_free``).  Returns pools."""
+    if stream is None and (_quick or _ready()):
+        dev = torch.cuda.current_device()
+        r = _quick.slot_free(pools, idx, live, dev, _raw_stream(dev))
+        if r is not None:
+            return _result(r, "gdr_slot_free")
     c = _Call(stream)
     arr, n_pools, slots = _pools(c, pools)
     pi = _list_i32(c, idx, "idx")

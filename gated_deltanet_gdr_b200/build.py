@@ -6,7 +6,9 @@ Each ``csrc/*.cu`` is compiled to an object with
 ``nvcc -gencode arch=compute_100a,code=sm_100a -O3 -lineinfo`` (in parallel) and
 linked into ``gated_deltanet_gdr_b200/libgdr.so`` with the CUDA runtime linked
 statically, so the library loads on a machine without a GPU driver (the driver is
-only opened at the first CUDA call).
+only opened at the first CUDA call).  ``csrc/marshal.cpp``, the checks and marshalling
+of the short calls for the Python binding, is compiled with g++ against the installed
+torch into ``_marshal.so``.
 """
 from __future__ import annotations
 
@@ -23,6 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdr.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xcompiler", "-Wall", "-diag-suppress", "177"]
@@ -45,10 +48,35 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    return _newer(LIB, _deps()) and _newer(MARSHAL, _marshal_deps())
+
+
+def _newer(target: str, deps) -> bool:
+    if not os.path.exists(target):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(p) <= t for p in deps)
+
+
+def _marshal_deps():
+    return [os.path.join(CSRC, "marshal.cpp"), os.path.join(INCLUDE, "gdr.h"), os.path.abspath(__file__)]
+
+
+def _build_marshal() -> None:
+    import sysconfig
+
+    import torch
+    root = os.path.join(os.path.dirname(torch.__file__))
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(root, "include"), "-isystem", os.path.join(root, "include/torch/csrc/api/include"),
+           os.path.join(CSRC, "marshal.cpp"), "-o", tmp, "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch",
+           "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling marshal.cpp failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
 
 
 def _compile(src: str, verbose_ptxas: bool) -> str:
@@ -67,10 +95,16 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if not force and up_to_date():
         return LIB
+    if not force and _newer(LIB, _deps()):
+        _build_marshal()
+        return LIB
     os.makedirs(OBJ, exist_ok=True)
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        marshal = None if not force and _newer(MARSHAL, _marshal_deps()) else ex.submit(_build_marshal)
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
+        if marshal is not None:
+            marshal.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", *objs, "-o", tmp, "-ldl", "-lpthread", "-lrt"]
     r = subprocess.run(cmd, capture_output=True, text=True)
