@@ -130,13 +130,15 @@ def lib() -> ctypes.CDLL:
 
 
 def _load_marshal(L) -> None:
-    """Loads _marshal.so and gives it the addresses of the C entries.  Without it (another torch than it was compiled
-    against, say) the short calls are marshalled in Python: the same checks and the same kernels, some microseconds
-    later."""
+    """Loads the extension _marshal and gives it the addresses of the C entries.  Without it, or with another torch than
+    it was compiled against (whose tensors may be laid out differently), the short calls are marshalled in Python: the
+    same checks and the same kernels, some microseconds later."""
     global _quick
     try:
         from . import _marshal as m
     except ImportError:
+        return
+    if m.torch_version != torch.__version__:
         return
     entries = ("gdr_scan_fwd", "gdr_scan_bwd", "gdr_scan_step", "gdr_conv1d_bwd", "gdr_conv1d_bwd_workspace",
                "gdr_slot_copy", "gdr_slot_fork", "gdr_slot_compact", "gdr_slot_free")

@@ -8,7 +8,7 @@ linked into ``gated_deltanet_gdr_b200/libgdr.so`` with the CUDA runtime linked
 statically, so the library loads on a machine without a GPU driver (the driver is
 only opened at the first CUDA call).  ``csrc/marshal.cpp``, the checks and marshalling
 of the short calls for the Python binding, is compiled with g++ against the installed
-torch into ``_marshal.so``.
+torch, as an extension module of the running Python (``_marshal``).
 """
 from __future__ import annotations
 
@@ -19,13 +19,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdr.so")
-MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL = os.path.join(PKG, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xcompiler", "-Wall", "-diag-suppress", "177"]
@@ -63,13 +64,12 @@ def _marshal_deps():
 
 
 def _build_marshal() -> None:
-    import sysconfig
-
     import torch
-    root = os.path.join(os.path.dirname(torch.__file__))
+    root = os.path.dirname(torch.__file__)
     tmp = MARSHAL + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-Wall",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", sysconfig.get_paths()["include"],
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DGDR_TORCH="{torch.__version__}"',
+           "-I", sysconfig.get_paths()["include"],
            "-isystem", os.path.join(root, "include"), "-isystem", os.path.join(root, "include/torch/csrc/api/include"),
            os.path.join(CSRC, "marshal.cpp"), "-o", tmp, "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch",
            "-ltorch_cpu", "-lc10"]
@@ -103,14 +103,14 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
         marshal = None if not force and _newer(MARSHAL, _marshal_deps()) else ex.submit(_build_marshal)
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
-        if marshal is not None:
-            marshal.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", *objs, "-o", tmp, "-ldl", "-lpthread", "-lrt"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    if marshal is not None:
+        marshal.result()
     return LIB
 
 

@@ -395,4 +395,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", "Marshalling of the sho
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal() { return PyModule_Create(&module); }
+// the version of torch whose headers this was compiled with, for the caller to compare before the first call
+PyMODINIT_FUNC PyInit__marshal() {
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "torch_version", GDR_TORCH) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

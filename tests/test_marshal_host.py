@@ -33,3 +33,13 @@ def test_wrong_numbers_of_arguments(m):
     for f in (m.scan_fwd, m.scan_bwd, m.scan_step, m.conv1d_bwd, m.slot_copy, m.slot_fork, m.slot_compact, m.slot_free, m.bind):
         with pytest.raises(TypeError):
             f(1)
+
+
+def test_another_torch_is_marshalled_in_python(m, monkeypatch):
+    L = gdr.lib()
+    monkeypatch.setattr(gdr, "_quick", None)
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    gdr._load_marshal(L)
+    assert gdr._quick is None
+    monkeypatch.undo()
+    assert m.torch_version == torch.__version__ and gdr._quick is m
