@@ -32,7 +32,9 @@ __device__ __forceinline__ void count_units(const SlotPools &p, Units &us) {
     __syncthreads();
 }
 
-// up to kBatch units in elements of U; src NULL: zeros
+// up to kBatch units in elements of U; src NULL: zeros.  What is written leaves the L2 cache first, so that sources which
+// several moves share stay (64 beams of 1.1 MB with random parents: 13.1 us a call, 14.9 with plain stores; 96 copies of 1.1
+// MB from random sources: 37.9 with either).
 template <typename U>
 __device__ __forceinline__ void move_elements(const char *src, char *dst, unsigned bytes) {
     const unsigned n = bytes / sizeof(U);
@@ -47,7 +49,7 @@ __device__ __forceinline__ void move_elements(const char *src, char *dst, unsign
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
-            if (i + k * kThreads < n) d[i + k * kThreads] = v[k];
+            if (i + k * kThreads < n) __stcs(d + i + k * kThreads, v[k]);
     }
 }
 
