@@ -269,9 +269,10 @@ __global__ void zero_f32_kernel(float *p, size_t n) {
     if (i < n) p[i] = 0.f;
 }
 
-// Tokens a warp walks: as many as pay for its beginning (4 x 4096 tokens of 8192 channels, us: bf16 168 with 128 tokens and 174
-// with 64, fp32 256 and 246).  Fewer, down to 16, where the blocks would not give every SM two -- the walk is the call's latency then, and the K - 1 tokens read twice cost
-// nothing (1 x 4096 tokens of 384 channels: 14 us with 32, 20 with 64) -- or where that leaves fewer warps without tokens.
+// Tokens a warp walks: as many as pay for its beginning (4 x 4096 tokens of 8192 channels, us: bf16 168 with 128 tokens
+// and 174 with 64, fp32 256 and 246).  Fewer, down to 16, where the blocks would not give every SM two -- the walk is
+// the call's latency then, and the K - 1 tokens read twice cost nothing (1 x 4096 tokens of 384 channels: 14 us with
+// 32, 20 with 64) -- or where that leaves fewer warps without tokens.
 int sub_for(int B, int S, int C, int most) {
     const long long groups = (long long)B * ((C + 32 * V - 1) / (32 * V));
     auto blocks = [&](int sub) { return (S + (long long)kWarps * sub - 1) / (kWarps * sub); };

@@ -130,12 +130,13 @@ struct Cut {
 };
 
 // The cut of the least estimated time.  A block spends about the same time on every tile, whatever its shape (a little
-// more with fewer lanes, for the shuffles; `wide` with 32, which need none), so a cut costs the tiles that a block walks through, times what the blocks of
-// the fullest SM cost together: 1 for one, 0.8 more for each of the up to `resident` that share it at a time.  A cluster
-// lies within one of the GPU's groups of SMs, which are not multiples of it: kFit, as the occupancy query reports it.
-// Measured, forward, us: 640 channels and 32769 tokens, 8 lanes: 59 with clusters of 6 (20 of the 22 that fit), 67 of 5, 72 of 8
-// (15 fit), 77 of 7; 128 rows of 128 channels and 4096 tokens: 92 with 32 lanes and 2 blocks, 93 with 16 and 1, 102 with 8 and 1; 64
-// channels and 65536 tokens: 45 with 4 lanes and 8 blocks, 77 with 8 lanes.
+// more with fewer lanes, for the shuffles; `wide` with 32, which need none), so a cut costs the tiles that a block
+// walks through, times what the blocks of the fullest SM cost together: 1 for one, 0.8 more for each of the up to
+// `resident` that share it at a time.  A cluster lies within one of the GPU's groups of SMs, which are not multiples of
+// it: kFit, as the occupancy query reports it. Measured, forward, us: 640 channels and 32769 tokens, 8 lanes: 59 with
+// clusters of 6 (20 of the 22 that fit), 67 of 5, 72 of 8 (15 fit), 77 of 7; 128 rows of 128 channels and 4096 tokens:
+// 92 with 32 lanes and 2 blocks, 93 with 16 and 1, 102 with 8 and 1; 64 channels and 65536 tokens: 45 with 4 lanes and
+// 8 blocks, 77 with 8 lanes.
 inline Cut choose_cut(long long rows, int D, int V, int S, int TS, int max_lx, int min_lx, int resident, double wide) {
     // clusters of 1 .. 8 blocks that a B200 of 148 SMs holds with one block on an SM
     constexpr int kFit[kMaxRanks] = {148, 74, 45, 33, 26, 22, 15, 15};

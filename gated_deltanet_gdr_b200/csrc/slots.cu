@@ -1,10 +1,11 @@
 // slots.cu -- copying, forking, compacting and freeing slots of the state pools (gdr_slot_copy, gdr_slot_fork,
 // gdr_slot_compact, gdr_slot_free).
 //
-// All four are moves of whole slots (or zero fills).  A slot is counted in units of kUnit bytes, and the units of all moves
-// are dealt out evenly, in runs, to the resident blocks.  Which slots move is worked out on the device: every block
-// derives the same plan from the index arrays in its own shared memory, so one launch does everything and the host never
-// waits for a count.  Bound by HBM: 128 slots of 1.1 MB copied (285 MB moved) in 45 us, 6.4 TB/s, 97 % of the measured copy rate.
+// All four are moves of whole slots (or zero fills).  A slot is counted in units of kUnit bytes, and the units of all
+// moves are dealt out evenly, in runs, to the resident blocks.  Which slots move is worked out on the device: every
+// block derives the same plan from the index arrays in its own shared memory, so one launch does everything and the
+// host never waits for a count.  Bound by HBM: 128 slots of 1.1 MB copied (285 MB moved) in 45 us, 6.4 TB/s, 97 % of
+// the measured copy rate.
 #include "common.cuh"
 #include "kernels.h"
 
