@@ -23,6 +23,8 @@ template <typename T, typename G, int V, bool kWide> struct Layout {
     float wa[2][kWarps][kCh], wb[2][kWarps][kCh];        // (A, B) of every warp, for even and odd tiles
     float ca[2][kMaxRanks][kCh], cb[2][kMaxRanks][kCh];  // (A, B) of every block of the cluster
     uint64_t arrived[2];                                 // their bytes
+    uint64_t closed;                                     // the bytes of sent[]
+    int sent[kMaxRanks];                                 // tiles that each block has sent to this one
 };
 
 template <typename T, typename G, bool kMix, int V, bool kWide, bool kRows>
@@ -60,12 +62,14 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
     const unsigned step = (unsigned)R * TT;  // tokens of the cluster's tiles; counted without sign, they may end past 2^31
     const int tiles = (int)((L + step - 1) / step);
     const unsigned exchange = (unsigned)(R * lx * V * 2 * sizeof(float));  // bytes of a tile's (A, B) of all blocks
-    bool lost = false;  // a wait ran out: no further waits
+    int got = tiles;  // tiles that this warp receives: fewer when a wait runs out
     if (R > 1) {
         if (tid == 0) {
             sm100::mbar_init(&sm.arrived[0], 1);
             sm100::mbar_init(&sm.arrived[1], 1);
+            sm100::mbar_init(&sm.closed, 1);
             sm100::fence_mbar_init();
+            sm100::mbar_arrive_expect_tx(&sm.closed, R * (unsigned)sizeof(int));
         }
         cluster_meet();  // every block of the cluster has started, with its barriers ready
     }
@@ -142,8 +146,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
         if (R > 1) {
             // the block as a whole to every block of the cluster, one warp for each.  A block writes a place again two
             // tiles on, having received the tile between, which its owner sent after reading this one.
-            if (tid == 0) sm100::mbar_arrive_expect_tx(&sm.arrived[p], exchange);
-            if (warp < R && lane < lx) {
+            if (tid == 0 && k <= got) sm100::mbar_arrive_expect_tx(&sm.arrived[p], exchange);
+            if (warp < R && lane < lx && k <= got) {
                 float2 ta[P], tb[P];
                 load_f32<V>(&sm.wa[p][0][cl * V], ta);
                 load_f32<V>(&sm.wb[p][0][cl * V], tb);
@@ -162,8 +166,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
                 put_remote<V>(&sm.cb[p][rank][cl * V], &sm.arrived[p], warp, tb);
             }
             __syncwarp();
-            if (!lost && !wait_remote(&sm.arrived[p], (unsigned)(k >> 1) & 1u, a.wait_ns)) {
-                lost = true;
+            if (k <= got && !__all_sync(0xffffffffu, wait_remote(&sm.arrived[p], (unsigned)(k >> 1) & 1u, a.wait_ns))) {
+                got = k;
                 raise_device_error(a.err, GDR_DEVERR_TIMEOUT);
             }
         }
@@ -223,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
             }
         }
     }
-    if (R > 1) cluster_meet();  // a block that gave up must not leave while the others write to it
+    if (R > 1 && warp < R && lane == 0) tell_sent(&sm.sent[rank], &sm.closed, warp, got < tiles ? got + 1 : tiles);
     if (!on) return;
     // tokens behind the last tile
     float2 zero[P];
@@ -231,6 +235,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs a,
     for (unsigned t = tiles * step + rank * (kThreads / lx) + seg; t < S; t += R * (kThreads / lx))
         store<T, V>(out + (size_t)t * row_x, zero);
     if (a.final_state && Lr >= 0 && seg == 0 && rank == 0) store<float, V>(a.final_state + (size_t)bn * a.D + c0, h);
+    // thread 0 is still here: a slab has one channel at least
+    if (R > 1 && tid == 0 && !all_landed(sm.arrived, &sm.closed, sm.sent, R, got, tiles, exchange / R, a.wait_ns))
+        raise_device_error(a.err, GDR_DEVERR_TIMEOUT);
 }
 
 template <typename T, typename G, bool kMix, int V, bool kWide, bool kRows>

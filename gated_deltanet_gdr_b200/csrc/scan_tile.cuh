@@ -117,6 +117,58 @@ __device__ __forceinline__ bool wait_remote(uint64_t *bar, unsigned parity, uint
     }
 }
 
+// ---- leaving a cluster ---------------------------------------------------------------------------------------------
+//
+// Warp w of a block sends its tiles' (A, B) to block w, and thread 0 counts what the block receives.  A warp whose wait for
+// a tile runs out waits for no later tile, sends none and (the first warp) counts none, but walks on through its tokens: so
+// the phase of an mbarrier is only ever begun with the phase before it complete.  A block leaves when every byte that the
+// others send to its shared memory has landed: at its end each warp tells its block how many tiles it has sent there, and
+// thread 0 waits for what is still on its way.
+
+constexpr uint64_t kDrainNs = 1000000000ull;  // more than a tile's limit that these waits are given: the others end theirs first
+
+// tells block `rank` that `tiles` tiles have been sent there (sent and closed given as this block's addresses)
+__device__ __forceinline__ void tell_sent(const int *sent, const uint64_t *closed, int rank, int tiles) {
+    unsigned a, b;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(sm100::smem_u32(sent)), "r"(rank));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(sm100::smem_u32(closed)), "r"(rank));
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(a), "r"(tiles), "r"(b)
+                 : "memory");
+}
+// Where a wait ran out: thread 0, having counted `mine` tiles, waits (bounded) until what every block r has sent to this
+// one, its tiles before sent[r], is there.  All tiles before mine - 1 have been received here.  The phase of tile mine - 1
+// expects the bytes of all blocks and gets those of the ones that sent it.  A warp sends tile t having received tile t - 1 of
+// all blocks; this block's warps send tile mine at most, since mine - 1 is the last one counted, so nobody sends more
+// than tile mine + 1: the phases of tiles mine and mine + 1 have only the bytes of the blocks ahead.  bytes: of one
+// block's (A, B) of a tile.
+static __device__ __noinline__ bool drain(uint64_t *arrived, const int *sent, int R, int mine, unsigned bytes, uint64_t limit_ns) {
+    for (int t = mine > 0 ? mine - 1 : 0; t < mine + 2; ++t) {
+        unsigned n = 0;  // blocks that sent tile t
+        for (int r = 0; r < R; ++r) n += sent[r] > t;
+        uint64_t *bar = &arrived[t & 1];
+        if (t >= mine) {
+            if (n == 0) break;
+            sm100::mbar_arrive_expect_tx(bar, n * bytes);
+        } else if (n < (unsigned)R) {
+            asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(sm100::smem_u32(bar)),
+                         "r"((R - n) * bytes)
+                         : "memory");
+        }
+        if (!wait_remote(bar, (unsigned)(t >> 1) & 1u, limit_ns)) return false;
+    }
+    return true;
+}
+// Thread 0 at a block's end: waits (bounded) until every byte sent to this block is there; false if a wait ran out.  got:
+// tiles that its warp has received
+__device__ __forceinline__ bool all_landed(uint64_t *arrived, uint64_t *closed, const int *sent, int R, int got, int tiles,
+                                           unsigned bytes, uint64_t limit_ns) {
+    limit_ns = limit_ns < ~0ull - kDrainNs ? limit_ns + kDrainNs : limit_ns;
+    if (!wait_remote(closed, 0u, limit_ns)) return false;
+    bool all = got == tiles;
+    for (int r = 0; r < R; ++r) all = all && sent[r] == tiles;
+    return all || drain(arrived, sent, R, got + 1 < tiles ? got + 1 : tiles, bytes, limit_ns);
+}
+
 // ---- the cut -------------------------------------------------------------------------------------------------------
 
 // whether rows are made of whole 16 bytes: tiles are then staged by warps
