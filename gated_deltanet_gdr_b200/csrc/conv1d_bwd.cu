@@ -130,7 +130,8 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, K>)) conv1d_bwd_kernel(c
             for (int i = 0; i < V; ++i) ds_in[i * K] = from_f32<T>(ds_out && L == 0 ? to_f32(ds_out[i * K]) : 0.f);
 
         // token u, at place j of the windows, its inputs at place p of stage s; whole: an ordinary one of the thread's
-        // tokens; halo: an ordinary one behind them
+        // tokens; halo: an ordinary one behind them.  What lies behind the sequence is told by its place, not by its zeros:
+        // the windows there still hold the last inputs, whose products may overflow.
         auto step = [&](int u, int j, int s, int p, bool whole, bool halo) {
             float2 g[P];
             unpack<T, V>(sm.x[s][p][tid], win[K - 1 + j]);
@@ -140,9 +141,9 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, K>)) conv1d_bwd_kernel(c
                 float2 pre = bias[i];
 #pragma unroll
                 for (int q = 0; q < K; ++q) pre = __ffma2_rn(w[q][i], win[j + q][i], pre);
-                const float2 d = __fmul2_rn(g[i], silu_slope(pre));
+                const float2 d = whole || halo || u < L ? __fmul2_rn(g[i], silu_slope(pre)) : both(0.f);
                 dwin[K - 1 + j][i] = d;
-                if (whole || (!halo && u < t1)) {
+                if (whole || (!halo && u < t1 && u < L)) {
                     db[i] = __fadd2_rn(db[i], d);
 #pragma unroll
                     for (int q = 0; q < K; ++q) dw[q][i] = __ffma2_rn(d, win[j + q][i], dw[q][i]);
@@ -156,6 +157,7 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, K>)) conv1d_bwd_kernel(c
 #pragma unroll
                 for (int q = 1; q < K; ++q) r[i] = __ffma2_rn(w[q][i], dwin[j + K - 1 - q][i], r[i]);
             }
+            if (!whole && !halo && max(t, 0) >= L) fill(r, 0.f);  // no token of the sequence takes part
             if (!whole && !halo && ds_out && t >= L - K && t < L) {
                 // the new state is the history from place L on: place q of it is position L - K + q
 #pragma unroll
@@ -183,17 +185,19 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, K>)) conv1d_bwd_kernel(c
                     dwin[j][i] = dwin[by + j][i];
                 }
         };
-        int s = 0;
+        const int ordinary = ds_out ? L - 1 : L;  // tokens before it complete none that takes part in the new state
+        const int reach = min(end, L + K - 1);    // tokens from here on complete padding only
+        int u = t0, s = 0;
 #pragma unroll 1
-        for (int u = t0; u < end; u += kBatch, s ^= 1) {
+        for (; u < reach; u += kBatch, s ^= 1) {
             stage_wait_but_one();
-            // every token of the batch is one of the thread's, and none that it completes lies before the sequence or
-            // takes part in the new state
-            if ((u > t0 || !first) && u + kBatch <= t1 && (!ds_out || u + kBatch < L)) {
+            // every token of the batch is one of the thread's and of the sequence, and none that it completes lies before
+            // the sequence or takes part in the new state
+            if ((u > t0 || !first) && u + kBatch <= t1 && u + kBatch <= ordinary) {
 #pragma unroll
                 for (int j = 0; j < kBatch; ++j) step(u + j, j, s, j, true, false);
                 shift(kBatch);
-            } else if (u == t1 && u >= t0 + kBatch && (!ds_out || u + K - 1 < L)) {  // the last K - 1
+            } else if (u == t1 && u >= t0 + kBatch && u + K - 1 <= ordinary) {  // the last K - 1
 #pragma unroll
                 for (int j = 0; j < K - 1; ++j) step(u + j, j, s, j, false, true);
             } else {
@@ -205,6 +209,9 @@ __global__ void __launch_bounds__(kThreads, (kBlocks<T, K>)) conv1d_bwd_kernel(c
             }
             fetch(u + 2 * kBatch, s);
         }
+        float2 zero[P];
+        fill(zero, 0.f);
+        for (int t = max(u - K + 1, t0); t < t1; ++t) store<T, V>(dx + (size_t)t * a.C, zero);
     }
     if (!a.partial) return;
     __shared__ float2 part[kWarps - 1][K + 1][P][32];
