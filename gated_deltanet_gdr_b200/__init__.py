@@ -496,10 +496,10 @@ class _Call:
         self.dev = torch.cuda.current_device()
         self.stream = _raw_stream(self.dev)
         self.other = None
+        if stream is not None and stream.device.index != self.dev:  # (default streams have one handle on every device)
+            raise RuntimeError(f"the stream is on {stream.device}, but the call runs on the current device "
+                               f"cuda:{self.dev}")
         if stream is not None and stream.cuda_stream != self.stream:
-            if stream.device.index != self.dev:
-                raise RuntimeError(f"the stream is on {stream.device}, but the call runs on the current device "
-                                   f"cuda:{self.dev}")
             self.other, self.stream, self.used = stream, stream.cuda_stream, []
 
     def ptr(self, t, name, dtype, shape):
