@@ -8,18 +8,22 @@ linked into ``gated_deltanet_gdr_b200/libgdr.so`` with the CUDA runtime linked
 statically, so the library loads on a machine without a GPU driver (the driver is
 only opened at the first CUDA call).  ``csrc/marshal.cpp``, the checks and marshalling
 of the short calls for the Python binding, is compiled with g++ against the installed
-torch, as an extension module of the running Python (``_marshal``).
+torch, as an extension module of the running Python (``_marshal``); where that fails, a
+warning says why, and the binding marshals those calls in Python.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
 import glob
+import hashlib
+import importlib.metadata
 import os
 import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
@@ -49,7 +53,7 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    return _newer(LIB, _deps()) and _newer(MARSHAL, _marshal_deps())
+    return _newer(LIB, _deps()) and _marshal_settled()
 
 
 def _newer(target: str, deps) -> bool:
@@ -59,11 +63,54 @@ def _newer(target: str, deps) -> bool:
     return all(os.path.getmtime(p) <= t for p in deps)
 
 
-def _marshal_deps():
+def _marshal_sources():
     return [os.path.join(CSRC, "marshal.cpp"), os.path.join(INCLUDE, "gdr.h"), os.path.abspath(__file__)]
 
 
+def _marshal_key() -> str:
+    """What the extension is made of: its sources and the torch whose headers it is compiled against."""
+    h = hashlib.sha256()
+    for p in _marshal_sources():
+        with open(p, "rb") as f:
+            h.update(f.read())
+    try:
+        torch_version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        torch_version = "none"
+    return f"{h.hexdigest()} torch {torch_version}"
+
+
+def _stamp() -> str:
+    return os.path.join(OBJ, "marshal.stamp")
+
+
+def _marshal_settled() -> bool:
+    """Whether the extension of this key was built and is there, or could not be built."""
+    try:
+        with open(_stamp()) as f:
+            key, outcome = f.read().rsplit(": ", 1)
+    except (OSError, ValueError):
+        return False
+    return key == _marshal_key() and (outcome == "failed" or os.path.exists(MARSHAL))
+
+
 def _build_marshal() -> None:
+    """Builds the extension, which the binding can do without: a failure is reported, and not tried again before something
+    changes (or with force)."""
+    os.makedirs(OBJ, exist_ok=True)
+    try:
+        _compile_marshal()
+        outcome = "built"
+    except Exception as e:
+        if os.path.exists(MARSHAL):
+            os.remove(MARSHAL)  # it may not fit the library any more
+        warnings.warn(f"the extension _marshal was not built (short calls are marshalled in Python; --force tries again): {e}")
+        outcome = "failed"
+    with open(_stamp(), "w") as f:
+        f.write(f"{_marshal_key()}: {outcome}")
+
+
+def _compile_marshal() -> None:
     import torch
     root = os.path.dirname(torch.__file__)
     tmp = MARSHAL + f".tmp{os.getpid()}"
@@ -101,7 +148,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     os.makedirs(OBJ, exist_ok=True)
     srcs = _sources()
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
-        marshal = None if not force and _newer(MARSHAL, _marshal_deps()) else ex.submit(_build_marshal)
+        marshal = None if not force and _marshal_settled() else ex.submit(_build_marshal)
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", *objs, "-o", tmp, "-ldl", "-lpthread", "-lrt"]
