@@ -9,6 +9,7 @@
 #include <cstring>
 #include <mutex>
 #include <unordered_map>
+#include <unordered_set>
 #include <vector>
 
 #include "../../include/gdr.h"
@@ -205,6 +206,59 @@ int check_decode_host(const int32_t *idx, const int32_t *lengths, const int32_t 
     return GDR_ERR_LAUNCH;
 }
 
+// Slot calls: what the kernels would skip and flag (an index out of range, a copy's target that is another copy's source or
+// target), and for a fork also a slot that two rows share.
+int check_copy_host(const int32_t *src, const int32_t *dst, int n, int slots, cudaStream_t s) try {
+    std::vector<int32_t> S, D;
+    if (!copy_i32(S, src, (size_t)n, s) || !copy_i32(D, dst, (size_t)n, s)) return GDR_ERR_LAUNCH;
+    auto moves = [&](int i) { return S[i] != -1 && D[i] != -1 && S[i] != D[i]; };
+    std::unordered_set<int32_t> targets;
+    for (int i = 0; i < n; ++i) {
+        if (!moves(i)) continue;
+        if (S[i] < 0 || S[i] >= slots || D[i] < 0 || D[i] >= slots) return GDR_ERR_SHAPE;
+        if (!targets.insert(D[i]).second) return GDR_ERR_SHAPE;
+    }
+    for (int i = 0; i < n; ++i)
+        if (moves(i) && targets.count(S[i])) return GDR_ERR_SHAPE;
+    return GDR_OK;
+} catch (...) {
+    return GDR_ERR_LAUNCH;
+}
+
+int check_fork_host(const int32_t *table, const int32_t *parents, int n, int slots, cudaStream_t s) try {
+    std::vector<int32_t> T, P;
+    if (!copy_i32(T, table, (size_t)n, s) || !copy_i32(P, parents, (size_t)n, s)) return GDR_ERR_LAUNCH;
+    auto in_range = [&](int32_t x) { return x >= 0 && x < slots; };
+    std::unordered_set<int32_t> seen;
+    std::vector<char> continued((size_t)n, 0);
+    std::vector<int> extra, dead;  // rows that take another row's slot, rows nobody continues from: as many
+    for (int i = 0; i < n; ++i) {
+        if (P[i] < -1 || P[i] >= n) return GDR_ERR_SHAPE;
+        if (in_range(T[i]) && !seen.insert(T[i]).second) return GDR_ERR_SHAPE;
+        if (P[i] >= 0 && !continued[P[i]]) continued[P[i]] = 1;
+        else extra.push_back(i);
+    }
+    for (int i = 0; i < n; ++i)
+        if (!continued[i]) dead.push_back(i);
+    for (size_t k = 0; k < extra.size(); ++k) {
+        const int32_t r = P[extra[k]];
+        if (r >= 0 && (!in_range(T[r]) || !in_range(T[dead[k]]))) return GDR_ERR_SHAPE;
+    }
+    return GDR_OK;
+} catch (...) {
+    return GDR_ERR_LAUNCH;
+}
+
+int check_free_host(const int32_t *idx, int n, int slots, cudaStream_t s) try {
+    std::vector<int32_t> I;
+    if (!copy_i32(I, idx, (size_t)n, s)) return GDR_ERR_LAUNCH;
+    for (int32_t x : I)
+        if (x < -1 || x >= slots) return GDR_ERR_SHAPE;
+    return GDR_OK;
+} catch (...) {
+    return GDR_ERR_LAUNCH;
+}
+
 // Whether no output shares bytes with an input or another output (spans without a pointer or without bytes share none)
 struct Span {
     const void *p;
@@ -392,8 +446,10 @@ extern "C" int gdr_conv1d(const void *x, const void *weight, const void *bias, c
     if (B == 0 || (S == 0 && !conv_state_out)) return GDR_OK;
     unsigned int *err = nullptr;
     if ((st = device_setup(&err))) return st;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (checks_enabled() && (st = check_lengths_host(actual_seq_lengths, B, S, cs))) return st;
     cudaError_t e = launch_conv1d(x, weight, bias, conv_state_in, actual_seq_lengths, B, S, Nk, Nv, Dk, Dv, K, dtype,
-                                  q, k, v, conv_state_out, err, reinterpret_cast<cudaStream_t>(stream));
+                                  q, k, v, conv_state_out, err, cs);
     return e == cudaSuccess ? GDR_OK : GDR_ERR_LAUNCH;
 }
 
@@ -595,8 +651,9 @@ extern "C" int gdr_slot_copy(const gdr_pool *pools, int n_pools, int slots, cons
     if (in_pools(p, src, n) || in_pools(p, dst, n)) return GDR_ERR_SHAPE;
     if (n == 0) return GDR_OK;
     if ((st = device_setup(&p.err))) return st;
-    return launch_slot_copy(p, src, dst, n, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? GDR_OK
-                                                                                                  : GDR_ERR_LAUNCH;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (checks_enabled() && (st = check_copy_host(src, dst, n, slots, cs))) return st;
+    return launch_slot_copy(p, src, dst, n, cs) == cudaSuccess ? GDR_OK : GDR_ERR_LAUNCH;
 }
 
 extern "C" int gdr_slot_fork(const gdr_pool *pools, int n_pools, int slots, const int32_t *slot_table,
@@ -613,8 +670,9 @@ extern "C" int gdr_slot_fork(const gdr_pool *pools, int n_pools, int slots, cons
     if (in_pools(p, slot_table, n) || in_pools(p, parents, n) || in_pools(p, new_slot_table, n)) return GDR_ERR_SHAPE;
     if (n == 0) return GDR_OK;
     if ((st = device_setup(&p.err))) return st;
-    return launch_slot_fork(p, slot_table, parents, n, new_slot_table, reinterpret_cast<cudaStream_t>(stream)) ==
-                   cudaSuccess ? GDR_OK : GDR_ERR_LAUNCH;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (checks_enabled() && (st = check_fork_host(slot_table, parents, n, slots, cs))) return st;
+    return launch_slot_fork(p, slot_table, parents, n, new_slot_table, cs) == cudaSuccess ? GDR_OK : GDR_ERR_LAUNCH;
 }
 
 extern "C" int gdr_slot_compact(const gdr_pool *pools, int n_pools, int slots, const int32_t *live, int32_t *new_slot,
@@ -645,8 +703,9 @@ extern "C" int gdr_slot_free(const gdr_pool *pools, int n_pools, int slots, cons
     if (in_pools(p, idx, n) || (live && in_pools(p, live, slots))) return GDR_ERR_SHAPE;
     if (n == 0) return GDR_OK;
     if ((st = device_setup(&p.err))) return st;
-    return launch_slot_free(p, idx, n, live, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? GDR_OK
-                                                                                                   : GDR_ERR_LAUNCH;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (checks_enabled() && (st = check_free_host(idx, n, slots, cs))) return st;
+    return launch_slot_free(p, idx, n, live, cs) == cudaSuccess ? GDR_OK : GDR_ERR_LAUNCH;
 }
 
 extern "C" int gdr_prologue_apply(const void *q, const void *k, const void *b, const float *a, const float *A_log,
