@@ -19,9 +19,7 @@ using namespace scan;
 constexpr int kSteps = 8;
 constexpr int kResident = 2;  // blocks of an SM
 
-// kWide: all 32 lanes of a warp lie over the channels, a segment is a warp and no shuffles are needed.  kCluster (below):
-// the blocks of a cluster share a sequence; a build of its own, for the registers (16 rows of 128 channels and 3000 tokens,
-// bf16, clusters of 8: 22.7 us, 24.7 with the number of blocks known at run time only).
+// kWide: all 32 lanes of a warp lie over the channels, a segment is a warp and no shuffles are needed
 template <typename T, typename G, int V, bool kWide> struct Layout {
     static constexpr int kCh = (kWide ? 32 : 16) * V;
     RawV<G, V> g[kSteps][kThreads];
@@ -34,7 +32,7 @@ template <typename T, typename G, int V, bool kWide> struct Layout {
     int sent[kMaxRanks];                                               // tiles that each block has sent to this one
 };
 
-template <typename T, typename G, bool kMix, int V, bool kWide, bool kRows, bool kCluster>
+template <typename T, typename G, bool kMix, int V, bool kWide, bool kRows>
 __global__ void __launch_bounds__(kThreads, kResident) scan_bwd_kernel(const ScanBwdArgs a, const Cut cut) {
     extern __shared__ __align__(16) unsigned char smem[];
     auto &sm = *reinterpret_cast<Layout<T, G, V, kWide> *>(smem);
@@ -42,7 +40,7 @@ __global__ void __launch_bounds__(kThreads, kResident) scan_bwd_kernel(const Sca
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int lx = kWide ? 32 : cut.lx, cl = lane & (lx - 1);
     const int seg = kWide ? warp : tid / lx;
-    const int R = kCluster ? cut.ranks : 1, rank = kCluster ? (int)(blockIdx.x % R) : 0;
+    const int R = cut.ranks, rank = (int)(blockIdx.x % R);
     const long long unit = blockIdx.x / R;
     const int slab = (int)(unit % cut.slabs);
     const long long bn = unit / cut.slabs;
@@ -72,7 +70,7 @@ __global__ void __launch_bounds__(kThreads, kResident) scan_bwd_kernel(const Sca
     const int chunk_warps = kSegs * lx > 32 ? kSegs * lx / 32 : 1;  // warps of a chunk: no warp holds more than one
     const unsigned exchange = (unsigned)(R * lx * V * 2 * sizeof(float));
     int got = tiles;  // tiles that this warp receives: fewer when a wait runs out
-    if (kCluster) {
+    if (R > 1) {
         if (tid == 0) {
             sm100::mbar_init(&sm.arrived[0], 1);
             sm100::mbar_init(&sm.arrived[1], 1);
@@ -180,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, kResident) scan_bwd_kernel(const Sca
             store<float, V>(&sm.wr[p][warp][cl * V], B);
         }
         __syncthreads();
-        if (kCluster) {  // as in the forward kernel, the block's backward map to every block of the cluster
+        if (R > 1) {  // as in the forward kernel, the block's backward map to every block of the cluster
             if (tid == 0 && n <= got) sm100::mbar_arrive_expect_tx(&sm.arrived[p], exchange);
             if (warp < R && lane < lx && n <= got) {
                 float2 ta[P], tb[P];
@@ -223,13 +221,13 @@ __global__ void __launch_bounds__(kThreads, kResident) scan_bwd_kernel(const Sca
                 h[i] = kMix ? __ffma2_rn(av[j][i], h[i], __fmul2_rn(xv[j][i], rest[kMix ? j : 0][i])) : __ffma2_rn(av[j][i], h[i], xv[j][i]);
                 xv[j][i] = q;
             }
-        if (kCluster && n <= got && !__all_sync(0xffffffffu, wait_remote(&sm.arrived[p], (unsigned)(n >> 1) & 1u, a.wait_ns))) {
+        if (R > 1 && n <= got && !__all_sync(0xffffffffu, wait_remote(&sm.arrived[p], (unsigned)(n >> 1) & 1u, a.wait_ns))) {
             got = n;
             raise_device_error(a.err, GDR_DEVERR_TIMEOUT);
         }
         // what comes back to this segment: from behind the tiles, the later blocks, the later warps, the later segments
         float2 m[P];
-        if (kCluster) {
+        if (R > 1) {
             for (int r = R - 1; r >= 0; --r) {
                 if (r == rank) {
 #pragma unroll
@@ -254,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, kResident) scan_bwd_kernel(const Sca
 #pragma unroll
             for (int i = 0; i < P; ++i) m[i] = __ffma2_rn(wa[i], m[i], wb[i]);
         }
-        if (!kCluster) {  // the whole tile: on through this warp and the earlier ones
+        if (R == 1) {  // the whole tile: on through this warp and the earlier ones
 #pragma unroll
             for (int i = 0; i < P; ++i) mu[i] = m[i];
 #pragma unroll
@@ -307,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, kResident) scan_bwd_kernel(const Sca
             }
         }
     }
-    if (kCluster && warp < R && lane == 0) tell_sent(&sm.sent[rank], &sm.closed, warp, got < tiles ? got + 1 : tiles);
+    if (R > 1 && warp < R && lane == 0) tell_sent(&sm.sent[rank], &sm.closed, warp, got < tiles ? got + 1 : tiles);
     if (!on) return;
     float2 zero[P];
     fill(zero, 0.f);
@@ -317,22 +315,17 @@ __global__ void __launch_bounds__(kThreads, kResident) scan_bwd_kernel(const Sca
     }
     if (a.dinitial_state && seg == 0 && rank == 0) store<float, V>(a.dinitial_state + (size_t)bn * a.D + c0, mu);
     // thread 0 is still here: a slab has one channel at least
-    if (kCluster && tid == 0 && !all_landed(sm.arrived, &sm.closed, sm.sent, R, got, tiles, exchange / R, a.wait_ns))
+    if (R > 1 && tid == 0 && !all_landed(sm.arrived, &sm.closed, sm.sent, R, got, tiles, exchange / R, a.wait_ns))
         raise_device_error(a.err, GDR_DEVERR_TIMEOUT);
-}
-
-template <typename T, typename G, bool kMix, int V, bool kWide, bool kRows, bool kCluster>
-cudaError_t launch_c(const ScanBwdArgs &a, const Cut &cut, cudaStream_t s) {
-    static LaunchCache cache(reinterpret_cast<const void *>(scan_bwd_kernel<T, G, kMix, V, kWide, kRows, kCluster>));
-    const int smem = (int)sizeof(Layout<T, G, V, kWide>);
-    const cudaError_t e = cache.allow_smem(smem);
-    if (e != cudaSuccess) return e;
-    return launch_clusters(scan_bwd_kernel<T, G, kMix, V, kWide, kRows, kCluster>, (long long)a.B * a.N, cut, smem, a, s);
 }
 
 template <typename T, typename G, bool kMix, int V, bool kWide, bool kRows>
 cudaError_t launch_v(const ScanBwdArgs &a, const Cut &cut, cudaStream_t s) {
-    return cut.ranks > 1 ? launch_c<T, G, kMix, V, kWide, kRows, true>(a, cut, s) : launch_c<T, G, kMix, V, kWide, kRows, false>(a, cut, s);
+    static LaunchCache cache(reinterpret_cast<const void *>(scan_bwd_kernel<T, G, kMix, V, kWide, kRows>));
+    const int smem = (int)sizeof(Layout<T, G, V, kWide>);
+    const cudaError_t e = cache.allow_smem(smem);
+    if (e != cudaSuccess) return e;
+    return launch_clusters(scan_bwd_kernel<T, G, kMix, V, kWide, kRows>, (long long)a.B * a.N, cut, smem, a, s);
 }
 
 template <typename T, typename G, bool kMix> cudaError_t launch_m(const ScanBwdArgs &a, cudaStream_t s) {
