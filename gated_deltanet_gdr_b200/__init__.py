@@ -534,10 +534,17 @@ class _Call:
             _check(status, what)
 
 
+def _int_sizes(shape, name):
+    """The sizes of a tensor that go to the C entries as int (ctypes would cut larger ones off)."""
+    if any(n >= 1 << 31 for n in shape):
+        raise ValueError(f"{name} must have sizes below 2^31, got {tuple(shape)}")
+    return shape
+
+
 def _sizes(x, name):
     if not isinstance(x, torch.Tensor) or x.dim() != 4:
         raise ValueError(f"{name} must be a (B, N, S, D) tensor")
-    return x.shape
+    return _int_sizes(x.shape, name)
 
 
 def _code(dt):
@@ -644,7 +651,7 @@ def _scan_step_args(x, g, state_pool, ssm_state_indices, actual_seq_lengths, num
         raise ValueError("state_pool must be a (slots, N, D) tensor")
     if not isinstance(ssm_state_indices, torch.Tensor) or ssm_state_indices.numel() != B * S:
         raise ValueError("ssm_state_indices must hold B * S int32 slot indices, one per flattened token")
-    slots = state_pool.shape[0]
+    slots = _int_sizes(state_pool.shape, "state_pool")[0]
     c = _Call(stream)
     px, pg = c.ptr(x, "x", dt, x.shape), c.ptr(g, "g", g.dtype, x.shape)
     pp = c.ptr(state_pool, "state_pool", torch.float32, (slots, N, D))
@@ -700,8 +707,8 @@ def conv1d_bwd(x, weight, dq, dk, dv, bias=None, conv_state=None, actual_seq_len
             return _result(r, "gdr_conv1d_bwd")
     if not isinstance(x, torch.Tensor) or x.dim() != 3 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("x must be (B, S, C) and weight (C, K)")
-    B, S, C = x.shape
-    K = weight.shape[1]
+    B, S, C = _int_sizes(x.shape, "x")
+    K = _int_sizes(weight.shape, "weight")[1]
     _, Nk, _, Dk = _sizes(dq, "dq")
     _, Nv, _, Dv = _sizes(dv, "dv")
     if C != 2 * Nk * Dk + Nv * Dv:
@@ -740,7 +747,7 @@ def _pools(c, pools):
         if not isinstance(t, torch.Tensor) or t.dim() < 1:
             raise ValueError("a pool must be a tensor whose first dimension is the slots")
         if slots is None:
-            slots = t.shape[0]
+            slots = _int_sizes(t.shape[:1], f"pools[{i}]")[0]
         elif t.shape[0] != slots:
             raise ValueError(f"all pools must have {slots} slots, pool {i} has {t.shape[0]}")
         arr[i].data = c.ptr(t, f"pools[{i}]", t.dtype, t.shape)
@@ -751,6 +758,7 @@ def _pools(c, pools):
 def _list_i32(c, t, name, n=None):
     if not isinstance(t, torch.Tensor) or t.dim() != 1:
         raise ValueError(f"{name} must be a one-dimensional int32 tensor")
+    _int_sizes(t.shape, name)
     return c.ptr(t, name, torch.int32, t.shape if n is None else (n,))
 
 
