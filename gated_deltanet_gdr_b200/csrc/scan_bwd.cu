@@ -3,9 +3,10 @@
 //
 // One pass over x, g and dout, last tile first (scan_tile.cuh).  mu is the same recurrence run backwards, so a span of
 // tokens composes forwards for h and backwards for mu with one product A.  The states come from the checkpoint before
-// each chunk of 64 tokens, so only mu is handed from tile to tile (and between the blocks of a cluster).  B=4 N=32 S=4096 D=128, bf16 with fp32
-// gates (941 MB): 156 us, 92 % of the measured copy rate, bound by HBM.  One sequence of 32769 tokens and 640 channels, fp16,
-// mixing (210 MB): 85 us, bound by a tile's latency.
+// each chunk of 64 tokens, so only mu is handed from tile to tile (and between the blocks of a cluster).  B=4 N=32 S=4096
+// D=128, bf16 with fp32 gates (941 MB): 160 us where the load makes the clocks fall, 90 % of the measured copy rate, and
+// 170 to 178 at full clocks, bound by HBM either way (what the blocks ask of the memory meets otherwise then).  One sequence of
+// 32769 tokens and 640 channels, fp16, mixing (210 MB): 83 us, bound by a tile's latency.
 #include "scan_tile.cuh"
 
 namespace gdr {

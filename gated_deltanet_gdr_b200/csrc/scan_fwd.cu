@@ -3,10 +3,10 @@
 //
 // One pass over x and g (scan_tile.cuh), 8 tokens of 4 channels a thread (fewer channels where rows are not made of
 // whole vectors).  The next tile's inputs are on their way (cp.async) while a tile is composed and written: two blocks
-// of 48 to 64 KB in flight an SM.  B=4 N=32 S=4096 D=128, bf16 with fp32 gates (537 MB): 95 us, 86 % of the measured
-// copy rate, bound by HBM with the issue slots at 55 %.  One sequence of 32769 tokens and 640 channels, fp16, mixing
-// (126 MB): 54 us, bound by a tile's latency: 11 rounds of clusters of 6, each a load, a composition, an exchange and a
-// store that wait for one another.
+// of 48 to 64 KB in flight an SM.  B=4 N=32 S=4096 D=128, bf16 with fp32 gates (537 MB): 96 us under sustained load, 85 %
+// of the measured copy rate (87 us in runs too short for the clocks to fall), bound by HBM with the issue slots at 57 %.
+// One sequence of 32769 tokens and 640 channels, fp16, mixing (126 MB): 55 us, bound by a tile's latency: 11 rounds of
+// clusters of 6, each a load, a composition, an exchange and a store that wait for one another.
 #include "scan_tile.cuh"
 
 namespace gdr {

@@ -4,8 +4,8 @@
 // One thread owns V channels of one sequence and keeps their state in registers over the tokens; the state is read once
 // and written once per commit, in 16-byte accesses where rows are made of whole ones.  The inputs of all tokens are
 // loaded before the slot index arrives, so a call waits for two memory round trips (index, state).  64 sequences of 4096
-// channels: 3.7 us on the device, 4.9 a call through the Python binding; 256 sequences of 4 drafts, fp16 (34 MB, 5 us at the
-// measured copy rate): 9.7 us, 10.2 with room for 8 tokens in registers.
+// channels: 2.4 us one after the other in a graph, 4.9 a call through the Python binding; 256 sequences of 4 drafts, fp16 (34
+// MB, 5 us at the measured copy rate): 7.9 us in a graph (8.7 with room for 8 tokens in registers), 9.7 to 10.2 a call.
 #include "kernels.h"
 #include "scan_tile.cuh"
 

@@ -175,7 +175,7 @@ __device__ __forceinline__ bool all_landed(uint64_t *arrived, uint64_t *closed, 
 template <typename T> bool rows_of_16(int D) { return D * (long long)sizeof(T) % 16 == 0; }
 
 struct Cut {
-    int lx;     // lanes side by side over the channels, a power of two from 2 to 32
+    int lx;     // lanes side by side over the channels, a power of two from 4 to 32
     int slabs;  // tiles over the channels
     int ranks;  // blocks of a cluster: consecutive tiles in time
     double estimate;
@@ -185,10 +185,11 @@ struct Cut {
 // more with fewer lanes, for the shuffles; `wide` with 32, which need none), so a cut costs the tiles that a block
 // walks through, times what the blocks of the fullest SM cost together: 1 for one, 0.8 more for each of the up to
 // `resident` that share it at a time.  A cluster lies within one of the GPU's groups of SMs, which are not multiples of
-// it: kFit, as the occupancy query reports it. Measured, forward, us: 640 channels and 32769 tokens, 8 lanes: 59 with
-// clusters of 6 (20 of the 22 that fit), 67 of 5, 72 of 8 (15 fit), 77 of 7; 128 rows of 128 channels and 4096 tokens:
-// 92 with 32 lanes and 2 blocks, 93 with 16 and 1, 102 with 8 and 1; 64 channels and 65536 tokens: 45 with 4 lanes and
-// 8 blocks, 77 with 8 lanes.
+// it: kFit, as the occupancy query reports it. Measured, forward, sustained, us: 640 channels and 32769 tokens, 4 lanes (40
+// clusters, at most two on an SM): 55 with clusters of 6 (22 fit side by side), 61 of 5, 76 of 7 and 81 of 8 (15 fit); 8
+// lanes (20 clusters): 57 of 6, 66 of 5, 71 of 8, 78 of 7; 128 rows of 128 channels and 4096 tokens: 96 with 32 lanes and 2
+// blocks, 103 with 16 and 1, 106 with 32 and 1, 110 with 8 and 1; 64 channels and 65536 tokens: 47 with 4 lanes and 8
+// blocks, 84 with 8 lanes.
 inline Cut choose_cut(long long rows, int D, int V, int S, int TS, int max_lx, int min_lx, int resident, double wide) {
     // clusters of 1 .. 8 blocks that a B200 of 148 SMs holds with one block on an SM
     constexpr int kFit[kMaxRanks] = {148, 74, 45, 33, 26, 22, 15, 15};
@@ -201,7 +202,7 @@ inline Cut choose_cut(long long rows, int D, int V, int S, int TS, int max_lx, i
     for (int lx = max_lx; lx >= min_lx; lx /= 2) {
         const long long slabs = (D + (long long)lx * V - 1) / ((long long)lx * V), clusters = rows * slabs;
         const long long tile = (long long)TS * (kThreads / lx);
-        const double shuffles = lx == 32 ? wide : lx == 16 ? 0.93 : lx == 8 ? 1.0 : lx == 4 ? 1.11 : 1.25;
+        const double shuffles = lx == 32 ? wide : lx == 16 ? 0.93 : lx == 8 ? 1.0 : 1.11;
         for (int r = 1; r <= kMaxRanks && (r == 1 || (r - 1) * tile < S); ++r) {
             const long long fit = kFit[r - 1] * sms >= 148 ? kFit[r - 1] * sms / 148 : 1;
             const double t = shuffles * (1.0 + 0.02 * r) * (double)((S + r * tile - 1) / (r * tile)) *

@@ -4,8 +4,8 @@
 // All four are moves of whole slots (or zero fills).  A slot is counted in units of kUnit bytes, and the units of all
 // moves are dealt out evenly, in runs, to the resident blocks.  Which slots move is worked out on the device: every
 // block derives the same plan from the index arrays in its own shared memory, so one launch does everything and the
-// host never waits for a count.  Bound by HBM: 128 slots of 1.1 MB copied (285 MB moved) in 45 us, 6.4 TB/s, 97 % of
-// the measured copy rate.
+// host never waits for a count.  Bound by HBM: 128 slots of 1.1 MB copied (285 MB moved) in 54 us a call, one call
+// after another, 5.3 TB/s, 80 % of the measured copy rate.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -34,8 +34,8 @@ __device__ __forceinline__ void count_units(const SlotPools &p, Units &us) {
 }
 
 // up to kBatch units in elements of U; src NULL: zeros.  What is written leaves the L2 cache first, so that sources which
-// several moves share stay (64 beams of 1.1 MB with random parents: 13.1 us a call, 14.9 with plain stores; 96 copies of 1.1
-// MB from random sources: 37.9 with either).
+// several moves share stay (96 copies of 1.1 MB from random sources, in a graph: 35.9 us, 36.2 with plain stores; 64 beams
+// with random parents: 13.2 with either).
 template <typename U>
 __device__ __forceinline__ void move_elements(const char *src, char *dst, unsigned bytes) {
     const unsigned n = bytes / sizeof(U);
@@ -77,7 +77,7 @@ __device__ __forceinline__ unsigned move_units(const SlotPools &p, const Units &
 }
 
 // Index lists of up to this many entries are read into shared memory once, so that what a block looks up between its moves
-// does not wait for memory (64 beams of 1.1 MB: 13.5 us on the device without this, 12.9 with it).
+// does not wait for memory (64 beams of 1.1 MB, in a graph: 13.5 us without this, 13.2 with it).
 constexpr int kCached = 4096;
 
 // both lists, from shared memory where they fit; the whole block takes part (and passes a barrier afterwards)

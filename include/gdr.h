@@ -367,9 +367,11 @@ size_t gdr_conv1d_bwd_workspace(int B, int S, int Nk, int Nv, int Dk, int Dv, in
  * to it, and a 16-bit state would drop them.
  *
  *   x                    device (B, N, S, D) in dtype (a channels-last (B, S, C) tensor is N = 1, D = C)
- *   g                    device (B, N, S, D) log-decay in gate_dtype: GDR_F32 or dtype.  -infinity forgets the state
- *                        exactly (a boundary between packed sequences).  Not range-checked: values above 0 grow the
- *                        state, and a run of tokens whose factors multiply past fp32 gives infinities or NaN
+ *   g                    device (B, N, S, D) log-decay in gate_dtype: GDR_F32 or dtype.  -infinity forgets a finite
+ *                        state exactly (a boundary between packed sequences).  Not range-checked: values above 0 grow the
+ *                        state, and a run of tokens whose factors multiply past fp32 gives infinities or NaN.  Spans
+ *                        of tokens are composed: an infinite state is NaN where the product of the decays behind it
+ *                        is below fp32, as with -infinity (0 times infinity), though no single decay is 0
  *   initial_state        device fp32 (B, N, D) or NULL: zeros
  *   actual_seq_lengths   device int32 (B) or NULL: all S.  Tokens t >= L_b are padding: their contents are ignored
  *                        and their out rows are zero.  L_b = 0 gives final_state = initial_state exactly
